@@ -1191,3 +1191,5 @@ extern "C" int hbl_forward_noalloc(const hbl_bf16* X, int M, int K, int N, const
   return forward_impl(X, M, K, N, Wpk, wscale, act_bits, use_hadamard, Y, ws, kNoAllocBytes,
                       reinterpret_cast<cudaStream_t>(stream), d);
 }
+
+#include "kv_api.cuh"

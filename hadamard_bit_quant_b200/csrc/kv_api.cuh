@@ -1,0 +1,172 @@
+// Host side of the paged 8-bit key/value cache: argument checks, workspace layout and launches. Included by
+// hbl_api.cu after its own helpers.
+#pragma once
+#include <cmath>
+#include "kv_cache.cuh"
+#include "kv_attn.cuh"
+
+namespace hbl {
+namespace {
+
+inline bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+// Pages of 16, 32, 64 or 128 tokens; slot numbers stay in an int32.
+int check_pages(int page, int num_pages) {
+  if (page != 16 && page != 32 && page != 64 && page != 128) return HBL_ERR_SHAPE;
+  if (num_pages < 1 || (long long)num_pages * page >= (1ll << 31)) return HBL_ERR_SHAPE;
+  return HBL_OK;
+}
+
+int check_heads(int T, int H, int D) {
+  if (T < 0 || H < 1 || H > 65535 || (D != 64 && D != 128)) return HBL_ERR_SHAPE;
+  if ((long long)T * H >= (1ll << 31)) return HBL_ERR_SHAPE;
+  return HBL_OK;
+}
+
+struct KvWs {
+  size_t prefix, ml, o, total;
+};
+
+KvWs kv_ws_layout(int B, int D) {
+  KvWs L;
+  size_t off = 0;
+  const size_t rows = (size_t)kv::kMaxAttnCtas * 2 * kv::kAttnRows;
+  L.prefix = off; off = align_up(off + ((size_t)B + 1) * 8, 256);
+  L.ml = off; off = align_up(off + rows * 8, 256);
+  L.o = off; off = align_up(off + rows * D * 4, 256);
+  L.total = off;
+  return L;
+}
+
+template <int D>
+int launch_kv_attention(const kv::AttnArgs& a, cudaStream_t s) {
+  ensure_smem_attr(kv::kv_attn_kernel<D>, kv::AttnCfg<D>::kSmem);
+  {
+    ProfScope ps("kv_attn", s);
+    launch_pdl(kv::kv_attn_kernel<D>, dim3(a.ctas), dim3(kv::kAttnWarps * 32), kv::AttnCfg<D>::kSmem, s, a);
+  }
+  {
+    ProfScope ps("kv_combine", s);
+    const long long rows = (long long)a.T * a.Hq;
+    launch_pdl(kv::kv_combine_kernel<D>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a);
+  }
+  return launch_status();
+}
+
+}  // namespace
+}  // namespace hbl
+
+extern "C" {
+
+int hbl_kv_plan(const int32_t* new_lens, int B, int page, int num_pages, int max_pages, int T, int32_t* kv_lens,
+                int32_t* block_table, int32_t* free_pages, int32_t* free_count, int32_t* cu_q, int32_t* slots,
+                int32_t* refused, hbl_stream stream) {
+  int st = check_pages(page, num_pages);
+  if (st) return st;
+  if (B < 0 || B > kv::kMaxRequests || T < 0 || max_pages < 1 || (long long)B * max_pages >= (1ll << 31) ||
+      (long long)max_pages * page >= (1ll << 31))
+    return HBL_ERR_SHAPE;
+  if (B == 0) return HBL_OK;
+  if (!new_lens || !kv_lens || !block_table || !free_pages || !free_count || !cu_q || !refused || (T > 0 && !slots))
+    return HBL_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)new_lens, (const void*)kv_lens, (const void*)block_table,
+                        (const void*)free_pages, (const void*)free_count, (const void*)cu_q, (const void*)slots,
+                        (const void*)refused})
+    if (misaligned(p, 4)) return HBL_ERR_INVALID_ARG;
+  DeviceState* d = nullptr;
+  if ((st = ensure_device(&d))) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const kv::PlanArgs a{new_lens, kv_lens, block_table, free_pages, free_count, cu_q, slots, refused,
+                       B, ilog2(page), num_pages, max_pages, T};
+  const size_t smem = 3 * ((size_t)B + 1) * 4;
+  ensure_smem_attr(kv::kv_plan_kernel, smem);
+  ProfScope ps("kv_plan", s);
+  kv::kv_plan_kernel<<<1, kv::kPlanThreads, smem, s>>>(a);
+  return launch_status();
+}
+
+int hbl_kv_append(const hbl_bf16* K, const hbl_bf16* V, int T, int Hkv, int D, long long k_stride,
+                  long long v_stride, const int32_t* slots, int page, int num_pages, uint8_t* kcodes,
+                  uint8_t* vcodes, float* kscale, float* vscale, hbl_stream stream) {
+  int st = check_pages(page, num_pages);
+  if (st || (st = check_heads(T, Hkv, D))) return st;
+  if (T == 0) return HBL_OK;
+  if (k_stride < (long long)Hkv * D || v_stride < (long long)Hkv * D || k_stride % 8 || v_stride % 8)
+    return HBL_ERR_SHAPE;
+  if (!K || !V || !slots || !kcodes || !vcodes || !kscale || !vscale) return HBL_ERR_INVALID_ARG;
+  if (misaligned16(K) || misaligned16(V) || misaligned16(kcodes) || misaligned16(vcodes)) return HBL_ERR_INVALID_ARG;
+  if (misaligned(slots, 4) || misaligned(kscale, 4) || misaligned(vscale, 4)) return HBL_ERR_INVALID_ARG;
+  DeviceState* d = nullptr;
+  if ((st = ensure_device(&d))) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const kv::AppendArgs a{{K, V}, {k_stride, v_stride}, {kcodes, vcodes}, {kscale, vscale}, slots, T, Hkv,
+                         ilog2(page), num_pages};
+  const dim3 grid((T + 7) / 8, Hkv, 2);
+  ProfScope ps("kv_append", s);
+  if (D == 64) launch_pdl(kv::kv_append_kernel<64>, grid, dim3(256), 0, s, a);
+  else launch_pdl(kv::kv_append_kernel<128>, grid, dim3(256), 0, s, a);
+  return launch_status();
+}
+
+int hbl_kv_read(const int32_t* slots, int T, int Hkv, int D, int page, int num_pages, const uint8_t* kcodes,
+                const uint8_t* vcodes, const float* kscale, const float* vscale, hbl_bf16* K, hbl_bf16* V,
+                hbl_stream stream) {
+  int st = check_pages(page, num_pages);
+  if (st || (st = check_heads(T, Hkv, D))) return st;
+  if (T == 0 || (!K && !V)) return HBL_OK;
+  if (!slots || (K && (!kcodes || !kscale)) || (V && (!vcodes || !vscale))) return HBL_ERR_INVALID_ARG;
+  if (misaligned16(K) || misaligned16(V) || misaligned16(kcodes) || misaligned16(vcodes)) return HBL_ERR_INVALID_ARG;
+  if (misaligned(slots, 4) || misaligned(kscale, 4) || misaligned(vscale, 4)) return HBL_ERR_INVALID_ARG;
+  DeviceState* d = nullptr;
+  if ((st = ensure_device(&d))) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const kv::ReadArgs a{{kcodes, vcodes}, {kscale, vscale}, {K, V}, slots, T, Hkv, ilog2(page), num_pages};
+  const dim3 grid((unsigned)(((long long)T * Hkv * (D / 8) + 255) / 256), 2);
+  ProfScope ps("kv_read", s);
+  if (D == 64) launch_pdl(kv::kv_read_kernel<64>, grid, dim3(256), 0, s, a);
+  else launch_pdl(kv::kv_read_kernel<128>, grid, dim3(256), 0, s, a);
+  return launch_status();
+}
+
+size_t hbl_kv_attention_workspace_bytes(int B, int D) {
+  if (B < 0 || (D != 64 && D != 128)) return 0;
+  return kv_ws_layout(B, D).total;
+}
+
+int hbl_kv_attention(const hbl_bf16* Q, int T, int Hq, int Hkv, int D, long long q_stride, const int32_t* cu_q,
+                     const int32_t* kv_lens, int B, int max_q, int max_kv, const int32_t* block_table,
+                     int max_pages, int page, int num_pages, const uint8_t* kcodes, const uint8_t* vcodes,
+                     const float* kscale, const float* vscale, float scale, int causal, int window, hbl_bf16* O,
+                     float* lse, void* ws, size_t ws_bytes, hbl_stream stream) {
+  int st = check_pages(page, num_pages);
+  if (st || (st = check_heads(T, Hq, D)) || (st = check_heads(T, Hkv, D))) return st;
+  if (Hq % Hkv != 0 || q_stride < (long long)Hq * D || q_stride % 8) return HBL_ERR_SHAPE;
+  if (B < 0 || B > kv::kMaxRequests || max_pages < 1 || (long long)B * max_pages >= (1ll << 31) ||
+      (long long)max_pages * page >= (1ll << 31))
+    return HBL_ERR_SHAPE;
+  if (max_q < 0 || max_kv < 0) return HBL_ERR_SHAPE;
+  if ((causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal)) return HBL_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return HBL_ERR_INVALID_ARG;
+  if (T == 0 || B == 0) return HBL_OK;
+  if (!Q || !cu_q || !kv_lens || !block_table || !kcodes || !vcodes || !kscale || !vscale || !O)
+    return HBL_ERR_INVALID_ARG;
+  if (misaligned16(Q) || misaligned16(kcodes) || misaligned16(vcodes) || misaligned16(O)) return HBL_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)cu_q, (const void*)kv_lens, (const void*)block_table, (const void*)kscale,
+                        (const void*)vscale, (const void*)lse})
+    if (misaligned(p, 4)) return HBL_ERR_INVALID_ARG;
+  const KvWs L = kv_ws_layout(B, D);
+  if (!ws || ws_bytes < L.total) return HBL_ERR_WORKSPACE;
+  if (misaligned(ws, 256)) return HBL_ERR_INVALID_ARG;
+  DeviceState* d = nullptr;
+  if ((st = ensure_device(&d))) return st;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  const kv::AttnArgs a{Q, q_stride, cu_q, kv_lens, block_table, kcodes, vcodes, kscale, vscale, O, lse,
+                       reinterpret_cast<long long*>(w + L.prefix), reinterpret_cast<float*>(w + L.ml),
+                       reinterpret_cast<float*>(w + L.o), scale * kv::kLog2e, T, Hq, Hkv, Hq / Hkv, B, max_pages,
+                       ilog2(page), num_pages, causal, window,
+                       d->sm_count < kv::kMaxAttnCtas ? d->sm_count : kv::kMaxAttnCtas};
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return D == 64 ? launch_kv_attention<64>(a, s) : launch_kv_attention<128>(a, s);
+}
+
+}  // extern "C"

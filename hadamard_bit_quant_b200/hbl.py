@@ -18,6 +18,7 @@ STATUS = {0: "HBL_OK", 1: "HBL_ERR_INVALID_ARG", 2: "HBL_ERR_SHAPE", 3: "HBL_ERR
 
 # (name, restype, argtypes) for every entry point of include/hbl.h
 _P, _I, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_L, _F = ctypes.c_longlong, ctypes.c_float
 SIGNATURES = [
     ("hbl_status_string", ctypes.c_char_p, [_I]),
     ("hbl_version", _I, []),
@@ -36,6 +37,12 @@ SIGNATURES = [
     ("hbl_pack_weights_rotated", _I, [_P, _I, _I, _P, _P, _P, _P]),
     ("hbl_hadamard_backward_f32", _I, [_P, _I, _I, _P, _P]),
     ("hbl_quantize_qkv", _I, [_P, _I, _I, _I, _I, _I, _P, _P, _P]),
+    ("hbl_kv_plan", _I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
+    ("hbl_kv_append", _I, [_P, _P, _I, _I, _I, _L, _L, _P, _I, _I, _P, _P, _P, _P, _P]),
+    ("hbl_kv_read", _I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P]),
+    ("hbl_kv_attention_workspace_bytes", _Z, [_I, _I]),
+    ("hbl_kv_attention", _I, [_P, _I, _I, _I, _I, _L, _P, _P, _I, _I, _I, _P, _I, _I, _I, _P, _P, _P, _P, _F, _I, _I,
+                              _P, _P, _P, _Z, _P]),
     ("hbl_selftest_wait_timeout", _I, [_I, _P, _P]),
     ("hbl_get_device_error", _I, [_P]),
     ("hbl_set_gemm_path", _I, [_I]),
@@ -168,6 +175,38 @@ def hbl_hadamard_backward_f32(dXr, M, K, dX, stream=None):
 def hbl_quantize_qkv(X, T, H, d, bits, bos_token, codes, gamma, stream=None):
     return _check(lib().hbl_quantize_qkv(_ptr(X), T, H, d, bits, bos_token, _ptr(codes), _ptr(gamma),
                                          _stream(stream)), "hbl_quantize_qkv")
+
+
+def hbl_kv_plan(new_lens, B, page, num_pages, max_pages, T, kv_lens, block_table, free_pages, free_count, cu_q, slots,
+                refused, stream=None):
+    return _check(lib().hbl_kv_plan(_ptr(new_lens), B, page, num_pages, max_pages, T, _ptr(kv_lens),
+                                    _ptr(block_table), _ptr(free_pages), _ptr(free_count), _ptr(cu_q), _ptr(slots),
+                                    _ptr(refused), _stream(stream)), "hbl_kv_plan")
+
+
+def hbl_kv_append(K, V, T, Hkv, D, k_stride, v_stride, slots, page, num_pages, kcodes, vcodes, kscale, vscale,
+                  stream=None):
+    return _check(lib().hbl_kv_append(_ptr(K), _ptr(V), T, Hkv, D, k_stride, v_stride, _ptr(slots), page, num_pages,
+                                      _ptr(kcodes), _ptr(vcodes), _ptr(kscale), _ptr(vscale), _stream(stream)),
+                  "hbl_kv_append")
+
+
+def hbl_kv_read(slots, T, Hkv, D, page, num_pages, kcodes, vcodes, kscale, vscale, K, V, stream=None):
+    return _check(lib().hbl_kv_read(_ptr(slots), T, Hkv, D, page, num_pages, _ptr(kcodes), _ptr(vcodes),
+                                    _ptr(kscale), _ptr(vscale), _ptr(K), _ptr(V), _stream(stream)), "hbl_kv_read")
+
+
+def hbl_kv_attention_workspace_bytes(B: int, D: int) -> int:
+    return lib().hbl_kv_attention_workspace_bytes(B, D)
+
+
+def hbl_kv_attention(Q, T, Hq, Hkv, D, q_stride, cu_q, kv_lens, B, max_q, max_kv, block_table, max_pages, page,
+                     num_pages, kcodes, vcodes, kscale, vscale, scale, causal, window, O, lse, ws, ws_bytes,
+                     stream=None):
+    return _check(lib().hbl_kv_attention(_ptr(Q), T, Hq, Hkv, D, q_stride, _ptr(cu_q), _ptr(kv_lens), B, max_q,
+                                         max_kv, _ptr(block_table), max_pages, page, num_pages, _ptr(kcodes),
+                                         _ptr(vcodes), _ptr(kscale), _ptr(vscale), scale, causal, window, _ptr(O),
+                                         _ptr(lse), _ptr(ws), ws_bytes, _stream(stream)), "hbl_kv_attention")
 
 
 def hbl_selftest_wait_timeout(timeout_us, gave_up=None, stream=None):

@@ -5,6 +5,8 @@ is in libhbl's kernels.
 """
 from __future__ import annotations
 
+from typing import NamedTuple
+
 import torch
 
 from . import hbl
@@ -78,3 +80,135 @@ class HBitLinear:
 
     def __call__(self, X: torch.Tensor, out=None, ws=None, stream=None) -> torch.Tensor:
         return forward(X, self.Wpk, self.wscale, self.N, self.act_bits, self.use_hadamard, out, ws, stream)
+
+
+class KVStep(NamedTuple):
+    """What one step of ``KVPages.plan`` wrote: a slot for each row, the requests' rows, who could not grow."""
+    slots: torch.Tensor
+    cu_q: torch.Tensor
+    refused: torch.Tensor
+
+
+def _index(*tensors):
+    for x in tensors:
+        assert x.is_cuda and x.dtype == torch.int32 and x.is_contiguous()
+
+
+class KVPages:
+    """Lengths, block table and free pages of a batch, shared by the caches of all layers.
+
+    kv_lens: int32 [B]; block_table: int32 [B, max_pages]; free_pages: int32 [num_pages], a stack whose first
+    free_count[0] entries are free. ``plan`` changes them in place.
+    """
+
+    def __init__(self, kv_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+                 free_count: torch.Tensor, page: int):
+        _index(kv_lens, block_table, free_pages, free_count)
+        assert block_table.dim() == 2 and block_table.shape[0] == kv_lens.numel() and free_count.numel() == 1
+        self.kv_lens, self.block_table = kv_lens, block_table
+        self.free_pages, self.free_count, self.page = free_pages, free_count, page
+
+    @classmethod
+    def empty(cls, requests: int, max_pages: int, num_pages: int, page: int, device="cuda") -> "KVPages":
+        """No tokens, every page free (page 0 is handed out first)."""
+        def full(*shape):
+            return torch.zeros(shape, dtype=torch.int32, device=device)
+        stack = torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device)
+        return cls(full(requests), full(requests, max_pages), stack, full(1) + num_pages, page)
+
+    def plan(self, new_lens: torch.Tensor, tokens: int, out: KVStep | None = None, stream=None) -> KVStep:
+        """Grow each request by new_lens[b] tokens (or drop -new_lens[b] of them): rows for ``tokens`` new ones."""
+        _index(new_lens)
+        B, max_pages = self.block_table.shape
+        assert new_lens.numel() == B and new_lens.device == self.kv_lens.device
+        if out is None:
+            new = new_lens.new_empty
+            out = KVStep(new(tokens), new(B + 1), new(B))
+        _index(*out)
+        assert out.slots.numel() == tokens and out.cu_q.numel() == B + 1 and out.refused.numel() == B
+        hbl.hbl_kv_plan(new_lens, B, self.page, self.free_pages.numel(), max_pages, tokens, self.kv_lens,
+                        self.block_table, self.free_pages, self.free_count, out.cu_q, out.slots, out.refused, stream)
+        return out
+
+
+class KVCache:
+    """One layer's paged 8-bit key/value cache.
+
+    kcodes, vcodes: uint8 [num_pages, kv_heads, page, head_dim]; kscale, vscale: fp32 [num_pages, kv_heads]. A
+    block stands for (codes - 128) * scale.
+    """
+
+    def __init__(self, kcodes: torch.Tensor, vcodes: torch.Tensor, kscale: torch.Tensor, vscale: torch.Tensor):
+        assert kcodes.dim() == 4 and kcodes.shape == vcodes.shape and kscale.shape == vscale.shape == kcodes.shape[:2]
+        for c, s in ((kcodes, kscale), (vcodes, vscale)):
+            assert c.is_cuda and s.device == c.device and c.dtype == torch.uint8 and s.dtype == torch.float32
+            assert c.is_contiguous() and s.is_contiguous()
+        self.kcodes, self.vcodes, self.kscale, self.vscale = kcodes, vcodes, kscale, vscale
+        self.num_pages, self.kv_heads, self.page, self.head_dim = kcodes.shape
+
+    @classmethod
+    def empty(cls, num_pages: int, kv_heads: int, page: int, head_dim: int, device="cuda") -> "KVCache":
+        shape = (num_pages, kv_heads, page, head_dim)
+        codes = [torch.full(shape, 128, dtype=torch.uint8, device=device) for _ in range(2)]
+        scales = [torch.zeros(shape[:2], dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(*codes, *scales)
+
+    def _rows(self, x: torch.Tensor, heads: int | None = None) -> int:
+        """Elements from token to token of a [tokens, heads, head_dim] tensor whose tokens may lie apart."""
+        assert x.is_cuda and x.dtype == torch.bfloat16 and x.dim() == 3 and x.device == self.kcodes.device
+        T, H, D = x.shape
+        assert D == self.head_dim and H == (heads or H)
+        assert x.stride(2) == 1 and (H == 1 or x.stride(1) == D)
+        return x.stride(0) if T > 1 else H * D
+
+    def append(self, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
+        """Quantise K and V (bf16 [T, kv_heads, head_dim], e.g. parts of one projection's output) into their slots."""
+        _index(slots)
+        ks, vs = self._rows(K, self.kv_heads), self._rows(V, self.kv_heads)
+        T = K.shape[0]
+        assert V.shape[0] == T and slots.numel() == T
+        hbl.hbl_kv_append(K, V, T, self.kv_heads, self.head_dim, ks, vs, slots, self.page, self.num_pages,
+                          self.kcodes, self.vcodes, self.kscale, self.vscale, stream)
+
+    def read(self, slots: torch.Tensor, stream=None):
+        """The values in the given slots: (K, V), bf16 [T, kv_heads, head_dim]."""
+        _index(slots)
+        T = slots.numel()
+        K, V = (torch.empty(T, self.kv_heads, self.head_dim, dtype=torch.bfloat16, device=self.kcodes.device)
+                for _ in range(2))
+        hbl.hbl_kv_read(slots, T, self.kv_heads, self.head_dim, self.page, self.num_pages, self.kcodes, self.vcodes,
+                        self.kscale, self.vscale, K, V, stream)
+        return K, V
+
+    def workspace(self, requests: int) -> torch.Tensor:
+        """Workspace of ``attention`` for a batch of that many requests."""
+        return torch.empty(hbl.hbl_kv_attention_workspace_bytes(requests, self.head_dim), dtype=torch.uint8,
+                           device=self.kcodes.device)
+
+    def attention(self, Q: torch.Tensor, cu_q: torch.Tensor, kv_lens: torch.Tensor, block_table: torch.Tensor,
+                  max_q: int = 0, max_kv: int = 0, scale: float | None = None, causal: bool = True, window: int = 0,
+                  out: torch.Tensor | None = None, return_lse: bool = False, lse: torch.Tensor | None = None,
+                  ws: torch.Tensor | None = None, stream=None):
+        """Attention of Q (bf16 [T, heads, head_dim]) over the cache: out, or (out, lse) with ``return_lse``.
+
+        Request b's rows are cu_q[b] .. cu_q[b + 1], its cache kv_lens[b] tokens in the pages block_table[b].
+        scale: 1 / sqrt(head_dim) unless given.
+        """
+        _index(cu_q, kv_lens, block_table)
+        stride = self._rows(Q)
+        T, Hq, D = Q.shape
+        B = kv_lens.numel()
+        assert cu_q.numel() == B + 1 and block_table.dim() == 2 and block_table.shape[0] == B
+        if out is None:
+            out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=Q.device)
+        assert out.shape == Q.shape and out.dtype == torch.bfloat16 and out.is_contiguous() and out.device == Q.device
+        if lse is None and return_lse:
+            lse = torch.empty(T, Hq, dtype=torch.float32, device=Q.device)
+        assert lse is None or (lse.shape == (T, Hq) and lse.dtype == torch.float32 and lse.is_contiguous())
+        if ws is None:
+            ws = self.workspace(B)
+        hbl.hbl_kv_attention(Q, T, Hq, self.kv_heads, D, stride, cu_q, kv_lens, B, max_q, max_kv, block_table,
+                             block_table.shape[1], self.page, self.num_pages, self.kcodes, self.vcodes, self.kscale,
+                             self.vscale, D ** -0.5 if scale is None else scale, int(causal), window, out, lse, ws,
+                             ws.numel(), stream)
+        return (out, lse) if return_lse else out

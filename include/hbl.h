@@ -260,6 +260,117 @@ int hbl_hadamard_backward_f32(const float* dXr, int M, int K, float* dX, hbl_str
 int hbl_quantize_qkv(const hbl_bf16* X, int T, int H, int d, int bits, int bos_token,
                      uint8_t* codes, float* gamma, hbl_stream stream);
 
+/* ------------------------------------------------------------------------
+ * The paged 8-bit key/value cache (section 3.4, "QKV Attention Quantization":
+ * post-RoPE keys and values kept as unsigned integers from their absmax) and
+ * attention over it.
+ *
+ * A cache holds num_pages pages of `page` consecutive tokens (16, 32, 64 or
+ * 128). For each key/value head a page is one block of page x D codes u and
+ * one scale s, and stands for the values (u - 128) * s:
+ *   kcodes, vcodes : device uint8, num_pages x Hkv x page x D.
+ *   kscale, vscale : device fp32, num_pages x Hkv.
+ * D is 64 or 128. A slot is a place for one token: page index * page + offset;
+ * num_pages * page < 2^31. Request b of a batch has kv_lens[b] tokens, token j
+ * in page block_table[b][j / page] (device int32, B x max_pages). All index
+ * arrays are device int32, their contents are read by the kernels only, and
+ * may change between replays of a captured call.
+ * Index arrays and scales need 4-byte alignment, everything else 16-byte.
+ * A page or slot outside the cache is skipped and recorded in the device
+ * error word (HBL_ERR_INVALID_ARG from hbl_get_device_error).
+ * None of these calls allocates or synchronises; all may be captured.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * hbl_kv_plan -- one step of the page table, from the requests' lengths.
+ *   new_lens   : device int32 B. >= 0: tokens that the request adds in this
+ *                step. < 0: tokens that it drops from its end (a rejected
+ *                draft); -kv_lens[b] or less releases the request.
+ *   kv_lens    : device int32 B, in/out: cached tokens before and after.
+ *   block_table: device int32 B x max_pages, in/out: entries of pages taken
+ *                are written, no other entry changes.
+ *   free_pages : device int32 num_pages, in/out: a stack whose first
+ *                *free_count entries are the free pages. Pages given back in
+ *                this step are handed out first (in the order of requests and
+ *                pages), then the stack from its top; what is left of them is
+ *                pushed with the first on top, so that dropping what a step
+ *                added restores the stack.
+ *   free_count : device int32 1, in/out.
+ *   cu_q       : device int32 B + 1, written: rows of each request's new
+ *                tokens (prefix sums of max(new_lens, 0), cut at T).
+ *   slots      : device int32 T, written: the slot of each row; -1 for rows of
+ *                refused requests and rows behind the last request. May be
+ *                NULL when T is 0.
+ *   refused    : device int32 B, written: 1 where the request could not grow
+ *                (more tokens than max_pages pages or than T rows; or the
+ *                pages ran out, then also for every later request that needs
+ *                a page). A refused request keeps its length and pages; its
+ *                rows in cu_q are of no use to attention.
+ * B <= 8192. Requests of one batch share no page that this step writes.
+ */
+int hbl_kv_plan(const int32_t* new_lens, int B, int page, int num_pages, int max_pages, int T,
+                int32_t* kv_lens, int32_t* block_table, int32_t* free_pages, int32_t* free_count,
+                int32_t* cu_q, int32_t* slots, int32_t* refused, hbl_stream stream);
+
+/*
+ * hbl_kv_append -- quantise new keys and values into their slots.
+ *   K, V   : device bf16, T tokens of Hkv x D, `k_stride` and `v_stride`
+ *            elements from one token to the next (>= Hkv * D, multiples of 8).
+ *   slots  : device int32 T; a negative slot is skipped.
+ * Tokens in consecutive slots of one page form a run. With gamma the run's
+ * absmax in a head, the block's scale becomes
+ *   s = max(s_before, gamma / 127, 2^-100)   (s_before = 0 if the run begins the page),
+ * codes that the block held before the run become rint(c * s_before / s), the
+ * new ones rint(x / s) (exact quotients, ties to even). NaN is stored as 0, an
+ * infinity as the largest finite value. Tokens that a page held behind the
+ * run are no longer valid. In one call a page may be named by one run only.
+ * T * Hkv < 2^31.
+ */
+int hbl_kv_append(const hbl_bf16* K, const hbl_bf16* V, int T, int Hkv, int D, long long k_stride,
+                  long long v_stride, const int32_t* slots, int page, int num_pages, uint8_t* kcodes,
+                  uint8_t* vcodes, float* kscale, float* vscale, hbl_stream stream);
+
+/*
+ * hbl_kv_read -- canonical view of the cache: the values bf16((u - 128) * s) in
+ * the named slots (zeros for a negative one). K, V: device bf16 T x Hkv x D,
+ * either may be NULL.
+ */
+int hbl_kv_read(const int32_t* slots, int T, int Hkv, int D, int page, int num_pages,
+                const uint8_t* kcodes, const uint8_t* vcodes, const float* kscale, const float* vscale,
+                hbl_bf16* K, hbl_bf16* V, hbl_stream stream);
+
+/* Bytes of caller workspace needed by hbl_kv_attention (it depends on B and D alone). */
+size_t hbl_kv_attention_workspace_bytes(int B, int D);
+
+/*
+ * hbl_kv_attention -- attention of new queries over the cache.
+ *   Q       : device bf16, T tokens of Hq x D, q_stride elements from one
+ *             token to the next (>= Hq * D, a multiple of 8). Hq is a multiple
+ *             of Hkv; query head i reads key/value head i / (Hq / Hkv).
+ *   cu_q    : device int32 B + 1, ascending: request b's rows are
+ *             [cu_q[b], cu_q[b + 1]), its last ones the last of its cache.
+ *   kv_lens : device int32 B: cached tokens, the new ones among them.
+ *   max_q, max_kv : bounds of a request's rows and cached tokens that the
+ *             caller knows (0: none); they choose kernels and never results.
+ *   scale   : finite, > 0; multiplies the scores.
+ *   causal  : 1: row i of q sees the keys up to position kv - q + i; 0: all.
+ *   window  : > 0 (with causal only): and of those the last `window`. 0: none.
+ *   O       : device bf16 T x Hq x D, written for the rows of the requests; rows
+ *             behind the last request are left as they were.
+ *   lse     : device fp32 T x Hq or NULL: log of the sum of exp(scale q.k).
+ *   ws      : device workspace, 256-byte aligned, clobbered; calls whose
+ *             execution overlaps must not share it.
+ * A row that sees no key gives zeros and an lse of -infinity. A key whose
+ * page is not in the cache counts as absent. Masked keys have no influence,
+ * whatever they hold. Scales must be finite. B <= 8192, T * Hq < 2^31.
+ */
+int hbl_kv_attention(const hbl_bf16* Q, int T, int Hq, int Hkv, int D, long long q_stride,
+                     const int32_t* cu_q, const int32_t* kv_lens, int B, int max_q, int max_kv,
+                     const int32_t* block_table, int max_pages, int page, int num_pages,
+                     const uint8_t* kcodes, const uint8_t* vcodes, const float* kscale,
+                     const float* vscale, float scale, int causal, int window, hbl_bf16* O, float* lse,
+                     void* ws, size_t ws_bytes, hbl_stream stream);
+
 /*
  * hbl_get_device_error -- synchronises `stream`, then reads and clears the
  * device error word that bounded waits inside the kernels set when they give

@@ -11,3 +11,4 @@ from .hbl_oracle import (EPS, SQRT7, INT4_RANGE, INT8_RANGE, TERN_RANGE, TIE_WIN
                          gemm_int, to_bf16, dequant, forward, forward_rows, RMS_EPS, rmsnorm, forward_ln,
                          rotate_weights, rotated_weight_quant, hadamard_backward, quantize_qkv,
                          dequantize_qkv)
+from .kv_oracle import KV_SCALE_FLOOR, kv_append, kv_attention, kv_plan, kv_read  # noqa: F401

@@ -1,0 +1,477 @@
+"""The paged 8-bit key/value cache on the GPU against the 64-bit oracle: page planning, appending, reading
+back, attention, and the four together as a serving loop uses them."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def L():
+    from hadamard_bit_quant_b200 import build, hbl, layer
+    build.build()
+    assert torch.cuda.is_available()
+    hbl.lib()
+    yield layer
+    assert hbl.hbl_get_device_error() == 0
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def np64(x):
+    return x.double().cpu().numpy()
+
+
+# ----------------------------------------------------------------------------- plan
+def random_state(rng, B, page, max_pages, spare):
+    """Lengths, a table and a stack of free pages, all pages somewhere."""
+    kv = rng.integers(0, max_pages * page + 1, B)
+    kv[rng.random(B) < 0.2] = 0
+    held = -(-kv // page)
+    num = int(held.sum()) + spare
+    order = rng.permutation(num)
+    table = rng.integers(0, num, (B, max_pages))
+    at = 0
+    for b in range(B):
+        table[b, :held[b]] = order[at:at + held[b]]
+        at += held[b]
+    free = np.full(num, -7)
+    free[:spare] = order[at:]
+    return kv, table, free, spare, num
+
+
+@pytest.mark.parametrize("B,page,max_pages,spare,most,T", [
+    (1, 16, 1, 1, 5, 5), (1, 128, 4, 3, 200, 512), (3, 16, 5, 0, 20, 64), (9, 32, 7, 6, 64, 300),
+    (40, 16, 9, 30, 40, 700), (33, 64, 3, 2, 90, 100), (257, 16, 12, 500, 60, 9000), (1500, 16, 4, 900, 9, 8000),
+    (8192, 16, 2, 4000, 3, 20000)])
+@pytest.mark.parametrize("seed", [0, 1])
+def test_plan(L, B, page, max_pages, spare, most, T, seed):
+    rng = np.random.default_rng(1000 * seed + B)
+    kv, table, free, count, num = random_state(rng, B, page, max_pages, spare)
+    pages = L.KVPages(i32(kv), i32(table), i32(free), i32([count]), page)
+    for step in range(3):
+        new = rng.integers(-most, most + 1, B)
+        new[rng.random(B) < 0.15] = 0
+        new[rng.random(B) < 0.05] = -2 ** 31
+        want = oracle.kv_plan(new, kv, table, free, count, page, T)
+        got = pages.plan(i32(new), T)
+        assert np.array_equal(got.cu_q.cpu(), want["cu_q"])
+        assert np.array_equal(got.refused.cpu(), want["refused"])
+        assert np.array_equal(got.slots.cpu(), want["slots"])
+        assert np.array_equal(pages.kv_lens.cpu(), want["kv_lens"])
+        assert np.array_equal(pages.block_table.cpu(), want["table"])
+        assert int(pages.free_count) == want["free_count"]
+        assert np.array_equal(pages.free_pages[:want["free_count"]].cpu(), want["free_pages"][:want["free_count"]])
+        kv, table, count = want["kv_lens"], want["table"], want["free_count"]
+        free = pages.free_pages.cpu().numpy()
+
+
+def test_plan_dropping_a_step_restores_the_stack(L):
+    rng = np.random.default_rng(3)
+    kv, table, free, count, num = random_state(rng, 20, 16, 10, 40)
+    pages = L.KVPages(i32(kv), i32(table), i32(free), i32([count]), 16)
+    new = np.minimum(rng.integers(0, 30, 20), 160 - kv)
+    step = pages.plan(i32(new), 600)
+    assert int(step.refused.sum()) == 0
+    pages.plan(i32(-new), 0)
+    assert np.array_equal(pages.kv_lens.cpu(), kv) and int(pages.free_count) == count
+    assert np.array_equal(pages.free_pages.cpu(), free)
+
+
+# ----------------------------------------------------------------------------- append and read
+def random_tokens(rng, T, H, D, kind):
+    x = rng.standard_normal((T, H, D))
+    if kind == "loud":
+        x[:, :, rng.integers(0, D, 3)] *= 60
+    elif kind == "ties":                 # halves of the absmax and of its steps: exact ties of x / s
+        x = rng.integers(-254, 255, (T, H, D)) * 0.5
+        x[:, :, 0] = 127
+    elif kind == "tiny":
+        x *= 1e-37
+    elif kind == "zero":
+        x[:] = 0
+    elif kind == "odd":                  # NaN, infinities, the largest and the smallest values
+        x[rng.random(x.shape) < 0.02] = np.nan
+        x[rng.random(x.shape) < 0.01] = np.inf
+        x[rng.random(x.shape) < 0.01] = -np.inf
+        x[rng.random(x.shape) < 0.05] = 3.38e38
+        x[rng.random(x.shape) < 0.05] = 1e-40
+    return torch.tensor(x, dtype=torch.float32).to(torch.bfloat16)
+
+
+def fresh_cache(L, rng, pages, H, page, D):
+    """A cache whose memory holds anything: random codes, scales from tiny to NaN."""
+    cache = L.KVCache.empty(pages, H, page, D)
+    for c in (cache.kcodes, cache.vcodes):
+        c.copy_(torch.tensor(rng.integers(0, 256, c.shape), dtype=torch.uint8))
+    for s in (cache.kscale, cache.vscale):
+        s.copy_(torch.tensor(rng.choice([0.0, 1e-3, 0.5, 40.0], s.shape), dtype=torch.float32))
+    return cache
+
+
+@pytest.mark.parametrize("H,D,page", [(1, 64, 16), (3, 128, 16), (5, 64, 128), (32, 128, 64), (8, 128, 32)])
+@pytest.mark.parametrize("kind", ["plain", "loud", "ties", "tiny", "zero", "odd"])
+def test_append_and_read(L, H, D, page, kind):
+    rng = np.random.default_rng(H + D + page)
+    num = 12
+    cache = fresh_cache(L, rng, num, H, page, D)
+    ref = [(c.cpu().numpy(), s.cpu().numpy()) for c, s in ((cache.kcodes, cache.kscale), (cache.vcodes, cache.vscale))]
+    order = rng.permutation(num)
+    # runs: (page, offset, tokens), page boundaries and skipped rows among them
+    steps = [[(0, 0, 1), (1, 0, page), (2, 0, page - 3), (3, 0, 2)],
+             [(0, 1, 1), (2, page - 3, 3), (4, 0, page), (3, 2, page - 5)],
+             [(0, 2, page - 2), (3, page - 3, 1), (5, 0, 7)]]
+    for i, runs in enumerate(steps):
+        slots = []
+        for p, off, n in runs:
+            slots += [int(order[p]) * page + off + k for k in range(n)] + ([-1] if i == 1 else [])
+        T = len(slots)
+        x = random_tokens(rng, T, 2 * H, D, kind) * (4.0 if i == 1 and kind == "plain" else 1.0)
+        xg = x.cuda()
+        K, V = xg[:, :H], xg[:, H:]                      # parts of one tensor: tokens lie apart
+        cache.append(K, V, i32(slots))
+        for j, (part, (codes, scale)) in enumerate(((K, ref[0]), (V, ref[1]))):
+            ref[j] = oracle.kv_append(np64(part), slots, codes, scale, page)
+    for (codes, scale), (c, s) in zip(ref, ((cache.kcodes, cache.kscale), (cache.vcodes, cache.vscale))):
+        assert np.array_equal(s.cpu().numpy(), scale)
+        assert np.array_equal(c.cpu().numpy(), codes)    # exact quotients: every code, and every byte not named
+    back = [-1] + [int(order[p]) * page + k for p in (0, 1, 2, 3, 4) for k in range(page)]
+    for got, (codes, scale) in zip(cache.read(i32(back)), ref):
+        want = torch.tensor(oracle.kv_read(back, codes, scale, page)).float().to(torch.bfloat16)
+        assert torch.equal(got.cpu(), want)
+
+
+def test_append_many_requests_of_one_token(L):
+    """Single tokens of 300 requests: every run is one token long, offsets of all kinds."""
+    rng = np.random.default_rng(8)
+    H, D, page, B = 2, 128, 16, 300
+    cache = fresh_cache(L, rng, B, H, page, D)
+    off = rng.integers(0, page, B)
+    slots = rng.permutation(B) * page + off
+    x = random_tokens(rng, B, 2 * H, D, "loud").cuda()
+    want = [oracle.kv_append(np64(p), slots, c.cpu().numpy(), s.cpu().numpy(), page)
+            for p, c, s in ((x[:, :H], cache.kcodes, cache.kscale), (x[:, H:], cache.vcodes, cache.vscale))]
+    cache.append(x[:, :H], x[:, H:], i32(slots))
+    for (codes, scale), (c, s) in zip(want, ((cache.kcodes, cache.kscale), (cache.vcodes, cache.vscale))):
+        assert np.array_equal(s.cpu().numpy(), scale) and np.array_equal(c.cpu().numpy(), codes)
+
+
+def test_append_a_prompt(L):
+    """One long prompt that begins inside a page; consecutive pages follow each other in the cache (one row of
+    slots without a gap must still be cut at the page ends)."""
+    rng = np.random.default_rng(9)
+    H, D, page, T = 3, 64, 32, 1000
+    cache = fresh_cache(L, rng, 40, H, page, D)
+    slots = np.arange(T) + 5 * page + 11
+    x = random_tokens(rng, T, 2 * H, D, "plain").cuda()
+    want = [oracle.kv_append(np64(p), slots, c.cpu().numpy(), s.cpu().numpy(), page)
+            for p, c, s in ((x[:, :H], cache.kcodes, cache.kscale), (x[:, H:], cache.vcodes, cache.vscale))]
+    cache.append(x[:, :H], x[:, H:], i32(slots))
+    for (codes, scale), (c, s) in zip(want, ((cache.kcodes, cache.kscale), (cache.vcodes, cache.vscale))):
+        assert np.array_equal(s.cpu().numpy(), scale) and np.array_equal(c.cpu().numpy(), codes)
+
+
+# ----------------------------------------------------------------------------- attention
+def close(got, lse, want, vmax, keys):
+    """Error bounds of one attention call, by element.
+
+    delta: a score is a sum of D products of exact fp16 values in fp32: D + 2 roundings of 2^-23 (the tensor
+    cores may truncate), relative to sum |q||k|; then a product and a difference in fp32. A probability is
+    off by that (twice, for the sum it is divided by), by 2^-11 for its rounding to fp16 and by 2^-25 at most
+    below fp16's normal range, where it is relative to the largest: that much of 127 vmax for each key, over a
+    sum of at least 1. The result is rounded to bf16, half a step.
+    """
+    out, ref_lse, mag, spread = want
+    D = out.shape[2]
+    got, lse = np64(got), np64(lse)
+    rows = ~np.isnan(ref_lse)
+    empty = np.isneginf(ref_lse)
+    assert np.array_equal(np.isneginf(lse[rows]), empty[rows])
+    finite = rows & ~empty
+    delta = spread * (D + 6) * 2.0 ** -23 + 2.0 ** -20
+    assert np.all(np.abs(lse[finite] - ref_lse[finite]) <= (delta + np.abs(np.where(finite, ref_lse, 0)) * 2.0 ** -21)[finite])
+    bound = 2.0 ** -8 * np.abs(out) + (2.0 ** -10 + 4 * delta[..., None]) * mag + 2.0 ** -25 * 127 * vmax * keys
+    err = np.abs(got - out)
+    assert np.all(err[rows] <= bound[rows]), float(np.nanmax((err - bound)[rows]))
+    assert np.all(got[empty] == 0)
+
+
+def make_case(L, seed, qs, kvs, Hq, Hkv, D, page, spare_rows=0, width=None, scale_spread=0.3):
+    rng = np.random.default_rng(seed)
+    B = len(qs)
+    counts = [-(-k // page) for k in kvs]
+    width = width or max(1, max(counts) + 1)
+    num = sum(counts) + 2
+    order = rng.permutation(num)
+    table = rng.integers(0, num, (B, width))
+    at = 0
+    for b in range(B):
+        table[b, :counts[b]] = order[at:at + counts[b]]
+        at += counts[b]
+    cache = L.KVCache.empty(num, Hkv, page, D)
+    for c in (cache.kcodes, cache.vcodes):
+        c.copy_(torch.tensor(np.clip(np.rint(rng.standard_normal(c.shape) * 32), -127, 127) + 128, dtype=torch.uint8))
+    for s in (cache.kscale, cache.vscale):
+        s.copy_(torch.tensor(np.exp(rng.standard_normal(s.shape) * scale_spread) * 0.03, dtype=torch.float32))
+    T = sum(qs) + spare_rows
+    cu = np.concatenate([[0], np.cumsum(qs)])
+    Q = torch.tensor(rng.standard_normal((T, Hq, D)) * 2, dtype=torch.float32).to(torch.bfloat16).cuda()
+    return cache, Q, cu, np.array(kvs), table
+
+
+def reference(cache, Q, cu, kvs, table, **kw):
+    return oracle.kv_attention(np64(Q), cu, kvs, table, cache.kcodes.cpu().numpy(), cache.vcodes.cpu().numpy(),
+                               cache.kscale.cpu().numpy(), cache.vscale.cpu().numpy(), cache.page,
+                               kw.pop("scale", cache.head_dim ** -0.5), **kw)
+
+
+def check(L, case, **kw):
+    cache, Q, cu, kvs, table = case
+    want = reference(*case, **kw)
+    out = torch.full_like(Q, 7.0)
+    lse = torch.full(Q.shape[:2], 7.0, device="cuda")
+    got, glse = cache.attention(Q, i32(cu), i32(kvs), i32(table), out=out, lse=lse, return_lse=True, **kw)
+    assert got is out and glse is lse
+    close(got, glse, want, float(cache.vscale.max()), int(np.max(kvs, initial=1)))
+    behind = np.isnan(want[1])
+    assert np.all(np64(got)[behind] == 7) and np.all(np64(glse)[behind] == 7)       # rows of no request: as they were
+    return got, glse
+
+
+HEADS = [(4, 4, 128, 16), (8, 1, 64, 32), (6, 2, 128, 64), (16, 1, 128, 128), (3, 3, 64, 16), (40, 2, 64, 64)]
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page", HEADS)
+def test_attention_single_tokens(L, Hq, Hkv, D, page):
+    kvs = [1, 2, page - 1, page, page + 1, 31, 32, 33, 257, 0, 700]
+    check(L, make_case(L, 1, [1] * len(kvs), kvs, Hq, Hkv, D, page))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page", HEADS)
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 1), (True, 40)])
+def test_attention_ragged_rows(L, Hq, Hkv, D, page, causal, window):
+    qs = [3, 0, 1, 17, 40, 5, 2, 8]
+    kvs = [3, 9, 300, 17, 90, 2, 0, 140]      # 5 rows over 2 keys and 2 over none: rows that see nothing
+    check(L, make_case(L, 2, qs, kvs, Hq, Hkv, D, page, spare_rows=3), causal=causal, window=window)
+
+
+@pytest.mark.parametrize("kv,Hq,Hkv,D,page", [(20011, 4, 1, 128, 16), (40000, 2, 2, 64, 64), (9973, 16, 1, 128, 128)])
+def test_attention_long_context_is_split(L, kv, Hq, Hkv, D, page):
+    check(L, make_case(L, 3, [1], [kv], Hq, Hkv, D, page))
+    check(L, make_case(L, 4, [2, 1], [kv // 2, 5], Hq, Hkv, D, page), window=kv // 3)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(4, 4, 128, 16), (4, 2, 64, 128), (8, 2, 128, 64), (5, 1, 128, 32)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 100)])
+def test_attention_prompts(L, Hq, Hkv, D, page, causal, window):
+    check(L, make_case(L, 5, [200, 333, 1, 64], [200, 500, 77, 70], Hq, Hkv, D, page, spare_rows=2), causal=causal,
+          window=window)
+
+
+def test_attention_hints_do_not_change_results(L):
+    case = make_case(L, 6, [1, 4, 150], [100, 900, 400], 8, 2, 128, 32)
+    got = [check(L, case, **kw) if not kw else case[0].attention(case[1], i32(case[2]), i32(case[3]), i32(case[4]),
+                                                                 return_lse=True, **kw)
+           for kw in ({}, {"max_q": 150, "max_kv": 900})]
+    want = reference(*case)
+    for o, l in got:
+        close(o, l, want, float(case[0].vscale.max()), 900)
+
+
+def test_attention_many_requests(L):
+    rng = np.random.default_rng(11)
+    kvs = rng.integers(0, 40, 700)
+    check(L, make_case(L, 7, rng.integers(0, 3, 700), kvs, 2, 1, 64, 16))
+
+
+def test_attention_scales_of_all_sizes(L):
+    """Block scales from 2^-60 to 2^40 side by side, queries from 1e-30 to 1e30."""
+    case = make_case(L, 8, [1, 1], [500, 90], 4, 2, 128, 16)
+    cache, Q = case[0], case[1]
+    rng = np.random.default_rng(5)
+    cache.vscale.copy_(torch.tensor(2.0 ** rng.integers(-60, 40, cache.vscale.shape), dtype=torch.float32))
+    check(L, case)
+    cache.vscale.fill_(0.03)
+    cache.kscale.mul_(1e30)
+    Q.copy_((Q.float() * 1e-30).to(torch.bfloat16))
+    check(L, case)
+    cache.kscale.mul_(1e-35)
+    cache.kscale.mul_(1e-25)
+    Q.copy_((Q.float() * 1e30).to(torch.bfloat16))
+    Q.mul_(1e30)
+    check(L, case)
+
+
+def test_attention_what_is_masked_has_no_influence(L):
+    """NaN and infinite scales of pages that no row sees, and rows behind the last key of a page."""
+    case = make_case(L, 9, [1, 2], [100, 300], 4, 2, 128, 16)
+    cache, Q, cu, kvs, table = case
+    first = [c.clone() for c in check(L, case, window=50)]
+    used = set()
+    for b, (lo, hi) in enumerate(((50, 100), (249, 300))):
+        used |= {int(table[b, j]) for j in range(lo // 16, -(-hi // 16))}
+    for p in range(cache.num_pages):
+        if p not in used:
+            cache.kscale[p], cache.vscale[p] = float("nan"), float("inf")
+            cache.kcodes[p], cache.vcodes[p] = 0, 255
+    again = cache.attention(Q, i32(cu), i32(kvs), i32(table), window=50, return_lse=True)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_attention_odd_queries(L):
+    """A NaN or an infinity in one row stays in that row; a row of zeros averages the values."""
+    case = make_case(L, 10, [4], [200], 2, 1, 64, 32)
+    cache, Q, cu, kvs, table = case
+    Q[1, 0, 3] = float("nan")
+    Q[2, 1, 5] = float("inf")
+    Q[3, 0] = 0
+    out, lse = cache.attention(Q, i32(cu), i32(kvs), i32(table), return_lse=True)
+    bad = torch.zeros(4, 2, dtype=torch.bool, device="cuda")
+    bad[1, 0] = bad[2, 1] = True
+    assert out[~bad].isfinite().all() and lse[~bad].isfinite().all()
+    assert out[1, 0].isnan().all() and lse[1, 0].isnan()
+    clean = Q.clone()
+    clean[1, 0, 3] = 0
+    clean[2, 1, 5] = 0
+    want = reference(cache, clean, cu, kvs, table)
+    want[1][bad.cpu().numpy()] = np.nan                      # not compared
+    close(out, lse, want, float(cache.vscale.max()), 200)
+
+
+def test_attention_query_as_part_of_a_projection(L):
+    case = make_case(L, 12, [3, 1], [60, 200], 4, 2, 64, 16)
+    cache, Q, cu, kvs, table = case
+    wide = torch.randn(4, 4 + 2 + 2, 64, device="cuda").to(torch.bfloat16)
+    wide[:, :4] = Q
+    want = cache.attention(Q, i32(cu), i32(kvs), i32(table), return_lse=True)
+    got = cache.attention(wide[:, :4], i32(cu), i32(kvs), i32(table), return_lse=True)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+def test_bad_pages_and_slots_are_skipped_and_recorded(L):
+    from hadamard_bit_quant_b200 import hbl
+    assert hbl.hbl_get_device_error() == 0
+    case = make_case(L, 13, [1, 2], [100, 200], 4, 2, 128, 16)
+    cache, Q, cu, kvs, table = case
+    table[0, 2], table[1, 5], table[1, 0] = -1, cache.num_pages, 2 ** 31 - 1
+    check(L, case)
+    assert hbl.hbl_get_device_error() == 1
+    assert hbl.hbl_get_device_error() == 0
+    before = [x.clone() for x in (cache.kcodes, cache.vcodes, cache.kscale, cache.vscale)]
+    x = torch.randn(2, 2, 128, device="cuda").to(torch.bfloat16)
+    cache.append(x, x, i32([cache.num_pages * 16, 2 ** 31 - 1]))
+    assert hbl.hbl_get_device_error() == 1
+    for a, b in zip(before, (cache.kcodes, cache.vcodes, cache.kscale, cache.vscale)):
+        assert torch.equal(a, b)
+    K, _ = cache.read(i32([cache.num_pages * 16, 3]))
+    assert hbl.hbl_get_device_error() == 1
+    assert bool((K[0] == 0).all())
+    # lengths beyond the table and rows beyond the queries are cut
+    out = cache.attention(Q, i32([0, 1, 900]), i32([2 ** 30, -5]), i32(np.abs(table) % cache.num_pages))
+    assert out[0].isfinite().all() and bool((out[1:] == 0).all())
+
+
+# ----------------------------------------------------------------------------- together
+def test_serving_loop(L):
+    """Requests arrive, decode, draft, are rejected and released; after every step the cache and the attention
+    over it are those of the oracle."""
+    rng = np.random.default_rng(21)
+    B, Hq, Hkv, D, page, num, width = 5, 4, 2, 64, 16, 24, 8
+    pages = L.KVPages.empty(B, width, num, page)
+    cache = L.KVCache.empty(num, Hkv, page, D)
+    ref = {"kv": np.zeros(B, int), "table": np.zeros((B, width), int), "free": np.arange(num)[::-1].copy(), "count": num}
+    codes = [(c.cpu().numpy(), s.cpu().numpy()) for c, s in ((cache.kcodes, cache.kscale), (cache.vcodes, cache.vscale))]
+    plans = [[40, 17, 0, 0, 1], [1, 1, 30, 0, 1], [1, 4, 1, 50, 1], [1, -3, 1, 1, -1], [-41, 1, 1, 1, 1],
+             [100, 4, 4, 4, 4], [-2 ** 31, 1, -33, 1, 1], [70, 1, 16, 1, 1]]
+    for new in plans:
+        T = sum(max(0, n) for n in new) + 2
+        step = pages.plan(i32(new), T)
+        want = oracle.kv_plan(np.array(new), ref["kv"], ref["table"], ref["free"], ref["count"], page, T)
+        ref = {"kv": want["kv_lens"], "table": want["table"], "free": want["free_pages"], "count": want["free_count"]}
+        assert np.array_equal(step.slots.cpu(), want["slots"]) and int(pages.free_count) == want["free_count"]
+        assert int(step.refused.sum()) == 0
+        qkv = torch.tensor(rng.standard_normal((T, Hq + 2 * Hkv, D)), dtype=torch.float32).to(torch.bfloat16).cuda()
+        Q, K, V = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+        cache.append(K, V, step.slots)
+        codes = [oracle.kv_append(np64(x), want["slots"], c, s, page) for x, (c, s) in zip((K, V), codes)]
+        out, lse = cache.attention(Q, step.cu_q, pages.kv_lens, pages.block_table, return_lse=True)
+        for (c, s), (gc, gs) in zip(codes, ((cache.kcodes, cache.kscale), (cache.vcodes, cache.vscale))):
+            assert np.array_equal(gc.cpu().numpy(), c) and np.array_equal(gs.cpu().numpy(), s)
+        close(out, lse, oracle.kv_attention(np64(Q), want["cu_q"], ref["kv"], ref["table"], codes[0][0], codes[1][0],
+                                            codes[0][1], codes[1][1], page, D ** -0.5), float(cache.vscale.max()),
+              int(max(1, ref["kv"].max())))
+
+
+def test_captured_step_replays_with_new_lengths(L):
+    """One decode step (plan, append, attention) captured once and replayed: lengths live on the GPU, so each replay
+    adds a token to every request."""
+    B, Hq, Hkv, D, page, num, width = 3, 8, 4, 128, 16, 40, 8
+
+    def make():
+        pages = L.KVPages.empty(B, width, num, page)
+        cache = L.KVCache.empty(num, Hkv, page, D)
+        g = torch.Generator(device="cuda").manual_seed(4)
+        x = torch.randn(40, 2 * Hkv, D, generator=g, device="cuda").to(torch.bfloat16)
+        step = pages.plan(i32([13, 20, 7]), 40)
+        cache.append(x[:, :Hkv], x[:, Hkv:], step.slots)
+        return pages, cache, g
+
+    one, qkv = i32([1] * B), torch.empty(B, Hq + 2 * Hkv, D, dtype=torch.bfloat16, device="cuda")
+
+    def decode(pages, cache, ws, out):
+        step = pages.plan(one, B)
+        cache.append(qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], step.slots)
+        return cache.attention(qkv[:, :Hq], step.cu_q, pages.kv_lens, pages.block_table, max_q=1, out=out, ws=ws)
+
+    pages, cache, g = make()
+    ws, out = cache.workspace(B), torch.empty(B, Hq, D, dtype=torch.bfloat16, device="cuda")
+    qkv.normal_(generator=g)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):                            # a call on another stream than the tensors' own
+        decode(pages, cache, ws, out)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        decode(pages, cache, ws, out)
+    outs = []
+    pages2, cache2, g2 = make()
+    g.manual_seed(99)
+    for i in range(20):
+        if i:
+            qkv.normal_(generator=g)
+        else:
+            # the eager copy takes the step that was run before the capture
+            g2.manual_seed(4)
+            torch.randn(40, 2 * Hkv, D, generator=g2, device="cuda")
+            keep = qkv.clone()
+            qkv.normal_(generator=g2)
+            decode(pages2, cache2, cache2.workspace(B), torch.empty_like(out))
+            qkv.copy_(keep)
+        graph.replay()
+        outs.append(out.clone())
+        eager = decode(pages2, cache2, cache2.workspace(B), torch.empty_like(out))
+        assert torch.equal(outs[-1], eager)
+    assert np.array_equal(pages.kv_lens.cpu(), [13 + 21, 20 + 21, 7 + 21])
+    assert torch.equal(cache.kcodes[pages.block_table[0, 0].item()], cache2.kcodes[pages2.block_table[0, 0].item()])
+
+
+def test_two_streams_with_workspaces_of_their_own(L):
+    case = make_case(L, 14, [1] * 4, [3000, 200, 5000, 1], 8, 2, 128, 64)
+    cache, Q, cu, kvs, table = case
+    args = i32(cu), i32(kvs), i32(table)
+    want = cache.attention(Q, *args)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for r in range(10):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(cache.attention(Q, *args, ws=cache.workspace(4)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
