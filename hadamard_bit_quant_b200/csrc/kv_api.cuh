@@ -1,9 +1,11 @@
 // Host side of the paged 8-bit key/value cache: argument checks, workspace layout and launches. Included by
 // hbl_api.cu after its own helpers.
 #pragma once
+#include <algorithm>
 #include <cmath>
 #include "kv_cache.cuh"
 #include "kv_attn.cuh"
+#include "kv_prefill.cuh"
 
 namespace hbl {
 namespace {
@@ -38,8 +40,24 @@ KvWs kv_ws_layout(int B, int D) {
   return L;
 }
 
+// Rows per key/value head up to which a request is streamed by kv_attn_kernel; more go to the tensor-core kernel.
+constexpr int kFewRows = 32;
+
+// Three kernels, each of which takes the requests that are its own: which those are is known on the GPU only.
+// The host leaves out what its bound on the rows rules out.
 template <int D>
 int launch_kv_attention(const kv::AttnArgs& a, cudaStream_t s) {
+  if (a.most_rows > a.few_rows) {
+    // every request wastes less than one tile of rows
+    const long long rows = (long long)a.T * a.group;
+    const long long items = rows / kv::kPreRows + std::min<long long>(a.B, rows / (a.few_rows + 1));
+    if (items > 0) {
+      const size_t smem = sizeof(kv::PreSmem<D>) + 1024;
+      ensure_smem_attr(kv::kv_prefill_kernel<D>, smem);
+      ProfScope ps("kv_prefill", s);
+      launch_pdl(kv::kv_prefill_kernel<D>, dim3((unsigned)(items * a.Hkv)), dim3(kv::kPreThreads), smem, s, a);
+    }
+  }
   ensure_smem_attr(kv::kv_attn_kernel<D>, kv::AttnCfg<D>::kSmem);
   {
     ProfScope ps("kv_attn", s);
@@ -47,8 +65,9 @@ int launch_kv_attention(const kv::AttnArgs& a, cudaStream_t s) {
   }
   {
     ProfScope ps("kv_combine", s);
-    const long long rows = (long long)a.T * a.Hq;
-    launch_pdl(kv::kv_combine_kernel<D>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a);
+    const int rows = std::min(a.few_rows, a.most_rows);
+    launch_pdl(kv::kv_combine_kernel<D>, dim3((unsigned)(((long long)a.B * a.Hkv * rows + 7) / 8)), dim3(256), 0, s, a,
+               rows);
   }
   return launch_status();
 }
@@ -164,7 +183,8 @@ int hbl_kv_attention(const hbl_bf16* Q, int T, int Hq, int Hkv, int D, long long
                        reinterpret_cast<long long*>(w + L.prefix), reinterpret_cast<float*>(w + L.ml),
                        reinterpret_cast<float*>(w + L.o), scale * kv::kLog2e, T, Hq, Hkv, Hq / Hkv, B, max_pages,
                        ilog2(page), num_pages, causal, window,
-                       d->sm_count < kv::kMaxAttnCtas ? d->sm_count : kv::kMaxAttnCtas};
+                       std::min(d->sm_count, kv::kMaxAttnCtas), std::max(kFewRows, Hq / Hkv),
+                       (int)std::min<long long>((long long)(max_q ? max_q : T) * (Hq / Hkv), 0x7fffffffll)};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return D == 64 ? launch_kv_attention<64>(a, s) : launch_kv_attention<128>(a, s);
 }

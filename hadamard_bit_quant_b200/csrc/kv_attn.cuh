@@ -49,21 +49,31 @@ struct AttnArgs {
   float* part_o;                      // workspace: [cta][2][16][D]
   float scale_log2;                   // softmax scale * log2(e)
   int T, Hq, Hkv, group, B, max_pages, page_log2, num_pages, causal, window, ctas;
+  int few_rows;                       // requests with more rows per key/value head than this go to kv_prefill_kernel
+  int most_rows;                      // and those with more than this break the caller's bound
 };
 
 // A request as the kernels see it: whatever the arrays hold, rows stay inside Q and keys inside the table.
-struct Request { int row0, q, kv, rt, lo, tiles; };
+struct Request {
+  int row0, q, kv;
+  int rt, lo, tiles;                  // for kv_attn_kernel: row tiles, first tile of keys, tiles of keys (0: not its request)
+  bool few;                           // rows that kv_attn_kernel takes
+};
 
 HBL_DEVINL Request request_of(const AttnArgs& a, int b) {
   Request r;
   r.row0 = min(max(a.cu_q[b], 0), a.T);
   r.q = min(max(a.cu_q[b + 1], r.row0), a.T) - r.row0;
   r.kv = (int)min((long long)max(a.kv_lens[b], 0), (long long)a.max_pages << a.page_log2);
+  r.few = (long long)r.q * a.group <= a.few_rows;
   r.rt = (int)(((long long)r.q * a.group + kAttnRows - 1) / kAttnRows);
   // tiles from the first key that any of its rows sees to the last
   r.lo = a.window > 0 ? max(r.kv - r.q + 1 - a.window, 0) / kAttnTile : 0;
-  r.tiles = r.q > 0 ? (r.kv + kAttnTile - 1) / kAttnTile - r.lo : 0;
+  r.tiles = r.q > 0 && r.few ? (r.kv + kAttnTile - 1) / kAttnTile - r.lo : 0;
   return r;
+}
+HBL_DEVINL bool prefill_request(const AttnArgs& a, const Request& r) {
+  return !r.few && (long long)r.q * a.group <= a.most_rows;
 }
 HBL_DEVINL long long tiles_of(const AttnArgs& a, const Request& r) { return (long long)r.tiles * r.rt * a.Hkv; }
 
@@ -510,23 +520,19 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) kv_attn_kernel(const AttnA
 }
 
 // Joins the parts of rows whose keys were split between CTAs, and writes the rows that see nothing at all.
-// One warp per (token, query head).
+// One warp per (request, key/value head, row), `rows` of them for each request and head.
 template <int D>
-__global__ void __launch_bounds__(256) kv_combine_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(256) kv_combine_kernel(const AttnArgs a, const int rows) {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= (long long)a.T * a.Hq) return;
-  const int t = (int)(row / a.Hq), head = (int)(row % a.Hq), h = head / a.group;
-  // the request that token t belongs to
-  int lo = 0, hi = a.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.cu_q[mid] <= t) lo = mid; else hi = mid;
-  }
+  const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lo = (int)(i / ((long long)rows * a.Hkv)), r = (int)(i % rows), h = (int)(i / rows % a.Hkv);
+  if (lo >= a.B) return;
   const Request rq = request_of(a, lo);
-  if (t < rq.row0 || t >= rq.row0 + rq.q) return;          // behind the last request
-  const int r = (t - rq.row0) * a.group + head % a.group, rt = r / kAttnRows;
+  if (r == 0 && h == 0 && lane == 0 && (long long)rq.q * a.group > a.most_rows) set_device_error(HBL_ERR_INVALID_ARG);
+  if (!rq.few || r >= rq.q * a.group) return;
+  const int rt = r / kAttnRows;
+  const size_t row = (size_t)(rq.row0 + r / a.group) * a.Hq + (size_t)(h * a.group + r % a.group);
   float M = -INFINITY, L = 0.f;
   constexpr int V = D / 32;                                 // channels of a lane
   float acc[V] = {};

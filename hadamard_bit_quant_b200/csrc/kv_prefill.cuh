@@ -1,0 +1,510 @@
+// Attention over the paged 8-bit key/value cache: many query rows per key/value head (prompts and chunks of
+// prompts), on the 5th-generation tensor cores.
+//
+// Same sums as kv_attn.cuh. Here the products bound it: 4 D multiply-add pairs for each row and key, beside
+// one exponential. One CTA takes 256 rows (query tokens times the heads that share a key/value head) of one
+// request and streams the keys in tiles of 128:
+//   * warps 8..11 read the codes, turn them into fp16 exactly and store them 128B-swizzled (keys and
+//     values have the same layout: token rows of 64 channels; the keys are read K-major, the values MN-major);
+//   * warp 12 issues tcgen05.mma kind::f16: S = Q K^T into TMEM, then O += P V with P as the A operand from TMEM;
+//   * warps 0..3 and 4..7 (a thread for each of 128 rows, twice) turn S into P in place. While one half's
+//     softmax runs, the tensor cores work for the other half: S, P and O of both fill the 512 TMEM columns.
+// A row's reference maximum is raised only when the running one has outgrown it by 2^8, and the values' reference
+// scale only when a block's scale is 16 times it, so the outputs in TMEM are rarely rescaled; probabilities
+// relative to such a reference stay below 2^12 and are rounded to fp16. A block's value scale enters as an addend of
+// the exponent (log2(s / reference)), which costs nothing; sums are fp32.
+// Every wait is bounded, as in gemm_tc.cuh.
+#pragma once
+#include "gemm_tc.cuh"
+#include "kv_attn.cuh"
+
+namespace hbl {
+namespace kv {
+
+constexpr int kPreRows = 256;            // query rows of a CTA, in two halves of 128
+constexpr int kPreKeys = 128;            // keys of a tile
+constexpr int kPreThreads = 512;
+constexpr int kPreGroups = kPreKeys / 16;
+constexpr int kPreRing = 4;              // tiles whose scales are held
+constexpr float kPreLag = 8.f;           // log2 of how far the running maximum may outgrow its reference
+constexpr float kPreSlack = 16.f;        // the same for the values' reference scale
+constexpr float kPreLeast = -60.f;       // log2 of the smallest scale, relative to the reference, that is told apart
+
+template <int D> struct __align__(1024) PreSmem {
+  static constexpr int kPanels = D / 64;
+  uint8_t q[2][kPanels][128 * 128];
+  uint8_t k[2][kPanels][kPreKeys * 128];
+  uint8_t v[2][kPanels][kPreKeys * 128];
+  // of each tile: [0, 8) key scales of the 16-key groups, [8, 16) log2 of their value scales relative to the
+  // reference, [16, 24) the inverses of those, [24] the reference, [25] bits of the groups that are not in the cache
+  float scale[kPreRing][32];
+  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
+  uint64_t drained;
+  long long sh[33];
+  int item_b;
+  int item_off;
+  uint32_t tmem_base;
+  int abort;
+};
+
+HBL_DEVINL void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accum)
+      : "memory");
+}
+HBL_DEVINL void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accum)
+      : "memory");
+}
+
+// Instruction descriptor: D fp32, A and B fp16, M = 128, N = n; bit 16: B is MN-major.
+HBL_DEVINL uint32_t idesc_f16(int n, bool b_mn) {
+  return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+// An MN-major 128B-swizzled tile: rows (k) of 128 bytes, 8-row groups 1024 bytes apart, the next 64 columns
+// `lead` bytes on.
+HBL_DEVINL uint64_t smem_desc_mn(uint32_t saddr, uint32_t lead) {
+  return (tc::smem_desc_sw128(saddr) & ~((uint64_t)0x3fff << 16)) | ((uint64_t)(lead >> 4) << 16);
+}
+
+#define HBL_TMEM_ST16(addr, r)                                                                                   \
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"   \
+               "%15,%16};\n" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),      \
+               "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),       \
+               "r"(r[14]), "r"(r[15])                                                                            \
+               : "memory")
+
+HBL_DEVINL void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+HBL_DEVINL void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// The keys that a half's rows see lie in the tiles [lo, hi).
+struct TileRange { int lo, hi; };
+HBL_DEVINL TileRange tiles_seen(const AttnArgs& a, const Request& rq, int row_a, int row_b) {
+  if (row_a > row_b) return {0, 0};
+  const int pos0 = rq.kv - rq.q;
+  const int last = a.causal ? min(rq.kv, pos0 + row_b / a.group + 1) : rq.kv;
+  const int first = a.window > 0 ? max(pos0 + row_a / a.group + 1 - a.window, 0) : 0;
+  if (last <= first) return {0, 0};
+  return {first / kPreKeys, (last + kPreKeys - 1) / kPreKeys};
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnArgs a) {
+  using S_t = PreSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  S_t& S = *reinterpret_cast<S_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort = &S.abort;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+
+  // the item of this CTA: request, head and row tile (longest first within a request)
+  auto items_of = [&](int b) {
+    const Request r = request_of(a, b);
+    return prefill_request(a, r) ? (long long)((r.q * (long long)a.group + kPreRows - 1) / kPreRows) * a.Hkv : 0ll;
+  };
+  {
+    const int per = (a.B + kPreThreads - 1) / kPreThreads;
+    const int b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) sum += items_of(b);
+    long long ex = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, ex, o);
+      if (lane >= o) ex += y;
+    }
+    if (lane == 31) S.sh[warp] = ex;
+    if (threadIdx.x == 0) S.item_b = -1;
+    __syncthreads();
+    for (int i = 0; i < warp; ++i) ex += S.sh[i];
+    ex -= sum;
+    if (ex <= blockIdx.x && blockIdx.x < ex + sum) {
+      long long x = ex;
+      for (int b = b0; b < b1; ++b) {
+        const long long n = items_of(b);
+        if (blockIdx.x < x + n) {
+          S.item_b = b;
+          S.item_off = (int)(blockIdx.x - x);
+          break;
+        }
+        x += n;
+      }
+    }
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&S.q_full[i], 128);
+      tc::mbar_init(&S.k_full[i], 128);
+      tc::mbar_init(&S.k_empty[i], 1);
+      tc::mbar_init(&S.v_full[i], 128);
+      tc::mbar_init(&S.v_empty[i], 1);
+      tc::mbar_init(&S.s_full[i], 1);
+      tc::mbar_init(&S.p_full[i], 128);
+      tc::mbar_init(&S.o_full[i], 1);
+    }
+    tc::mbar_init(&S.drained, 1);
+    S.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  __syncthreads();
+  if (S.item_b < 0) return;
+  const int b = S.item_b;
+  const Request rq = request_of(a, b);
+  const int nrows = rq.q * a.group;
+  const int rts = (nrows + kPreRows - 1) / kPreRows;
+  const int rt = rts - 1 - S.item_off / a.Hkv, h = S.item_off % a.Hkv;
+  const int row0 = rt * kPreRows;
+  TileRange half[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+    half[w] = tiles_seen(a, rq, row0 + 128 * w, min(row0 + 128 * w + 127, nrows - 1));
+  // tiles of the CTA; a half without keys has an empty range
+  int lo = 0x7fffffff, hi = 0;
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+    if (half[w].lo < half[w].hi) {
+      lo = min(lo, half[w].lo);
+      hi = max(hi, half[w].hi);
+    }
+  if (warp == 12) {
+    tc::tmem_alloc(&S.tmem_base, 512);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+
+  if (warp < 8) {
+    // ----- a row's softmax -----
+    const int w = warp >> 2;
+    const int r = row0 + 128 * w + (threadIdx.x & 127);
+    const bool live = r < nrows;
+    const int tok = min(r, nrows - 1) / a.group, head = h * a.group + min(r, nrows - 1) % a.group;
+    const int pos = rq.kv - rq.q + tok;
+    const int last = a.causal ? max(min(rq.kv, pos + 1), 0) : rq.kv;
+    const int first = a.window > 0 ? max(pos + 1 - a.window, 0) : 0;
+    float qs;
+    {
+      // the row in fp16, brought into its range by a power of two, to shared memory
+      const uint4* src = reinterpret_cast<const uint4*>(a.Q + (size_t)(rq.row0 + tok) * (size_t)a.q_stride + (size_t)head * D);
+      float amax = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = __ldg(src + c);
+        const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(ws[k] << 16)), fabsf(__uint_as_float(ws[k] & 0xffff0000u))));
+      }
+      float up;
+      row_power(amax, &up, &qs);
+      qs *= a.scale_log2;
+      const int rr = threadIdx.x & 127;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = __ldg(src + c);
+        const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          o[k] = pack_half(__uint_as_float(ws[k] << 16) * up, __uint_as_float(ws[k] & 0xffff0000u) * up);
+        sts128(tc::su32(&S.q[w][c >> 3][rr * 128 + (((c & 7) ^ (rr & 7)) << 4)]), make_uint4(o[0], o[1], o[2], o[3]));
+      }
+      fence_async_smem();
+      tc::mbar_arrive(&S.q_full[w]);
+    }
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t s_addr = lane_base + (uint32_t)(128 * w), o_addr = lane_base + (uint32_t)(256 + 128 * w);
+    // keys that every row of this warp sees, for the tiles that need no mask
+    const int lane_lo = __reduce_max_sync(0xffffffffu, first), lane_hi = __reduce_min_sync(0xffffffffu, last);
+    float m = -INFINITY, l = 0.f, vref = 0.f;
+    bool ok = true;
+    for (int j = half[w].lo; j < half[w].hi; ++j) {
+      const int n = j - half[w].lo;
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(&S.s_full[w], (uint32_t)n & 1u, abort));
+      if (!ok) break;
+      tc::tc_fence_after();
+      const uint32_t sc = tc::su32(&S.scale[(j - lo) % kPreRing][0]);
+      float f[kPreGroups], add[kPreGroups];
+#pragma unroll
+      for (int g = 0; g < kPreGroups; g += 4) {
+        const uint4 x = lds128(sc + 4 * g), y = lds128(sc + 32 + 4 * g);
+        f[g] = __uint_as_float(x.x); f[g + 1] = __uint_as_float(x.y);
+        f[g + 2] = __uint_as_float(x.z); f[g + 3] = __uint_as_float(x.w);
+        add[g] = __uint_as_float(y.x); add[g + 1] = __uint_as_float(y.y);
+        add[g + 2] = __uint_as_float(y.z); add[g + 3] = __uint_as_float(y.w);
+      }
+      const float vnow = lds32f(sc + 96);
+      const uint32_t bad = __float_as_uint(lds32f(sc + 100));
+#pragma unroll
+      for (int g = 0; g < kPreGroups; ++g) f[g] *= qs;
+      const int key0 = j * kPreKeys;
+      const bool whole = key0 >= lane_lo && key0 + kPreKeys <= lane_hi && bad == 0;
+      // columns [c_lo, c_hi) are seen by this row
+      const int c_lo = first - key0, c_hi = last - key0;
+      float mt = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t x[32];
+        HBL_TMEM_LD32(s_addr + 32u * c, x);
+        tc::tc_wait_ld();
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (32 * c + i < c_lo || 32 * c + i >= c_hi || (bad >> (2 * c + (i >> 4))) & 1) x[i] = 0xff800000u;
+          HBL_TMEM_ST32(s_addr + 32u * c, x);                // masked for the second reading too
+        }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          float y = __uint_as_float(x[16 * g]);
+#pragma unroll
+          for (int i = 1; i < 16; ++i) y = fmaxf(y, __uint_as_float(x[16 * g + i]));
+          mt = fmaxf(mt, y * f[2 * c + g]);
+        }
+      }
+      if (!whole) tc::tc_wait_st();
+      const float mn = mt > m + kPreLag ? mt : m;
+      const float alpha = mn == m ? 1.f : exp2_fast(m - mn);
+      const float shrink = vref == vnow ? 1.f : __fdividef(vref, vnow);
+      vref = vnow;
+      m = mn;
+      l *= alpha;
+      const float ao = alpha * shrink;
+      if (n > 0 && __any_sync(0xffffffffu, ao != 1.f)) {
+        // the products so far are complete: the scores of this tile were issued behind them
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t x[32];
+          HBL_TMEM_LD32(o_addr + 32u * c, x);
+          tc::tc_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * ao);
+          HBL_TMEM_ST32(o_addr + 32u * c, x);
+        }
+      }
+      const float mu = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t x[32], p[16];
+        HBL_TMEM_LD32(s_addr + 32u * c, x);
+        tc::tc_wait_ld();
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const float ff = f[2 * c + g], aa = add[2 * c + g] - mu;
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float e = exp2_fast(__fmaf_rn(__uint_as_float(x[16 * g + i]), ff, aa));
+            sum += e;
+            x[16 * g + i] = __float_as_uint(e);
+          }
+          l = __fmaf_rn(sum, lds32f(sc + 64 + 4 * (2 * c + g)), l);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) p[i] = pack_half(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+        HBL_TMEM_ST16(s_addr + 16u * c, p);
+      }
+      tc::tc_wait_st();
+      tc::tc_fence_before();
+      tc::mbar_arrive(&S.p_full[w]);
+    }
+    // ----- the row's output -----
+    const bool any = half[w].lo < half[w].hi;
+    if (any) ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(&S.o_full[w], 0, abort));
+    if (ok && !*abort) {
+      tc::tc_fence_after();
+      const bool some = l > 0.f || l != l;
+      const float inv = some ? vref / l : 0.f;
+      const size_t out = (size_t)(rq.row0 + tok) * a.Hq + head;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t x[32];
+        if (any) {
+          HBL_TMEM_LD32(o_addr + 32u * c, x);
+          tc::tc_wait_ld();
+        }
+        if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(a.O + out * D + 32 * c);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float e0 = some ? __uint_as_float(x[8 * k + 2 * i]) * inv : 0.f;
+              const float e1 = some ? __uint_as_float(x[8 * k + 2 * i + 1]) * inv : 0.f;
+              y[i] = (uint32_t)float_to_bf16_bits(e0) | ((uint32_t)float_to_bf16_bits(e1) << 16);
+            }
+            dst[k] = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        }
+      }
+      if (live && a.lse) a.lse[out] = some ? m * kLn2 + logf(l) : -INFINITY;
+    }
+  } else if (warp < 12) {
+    // ----- codes to fp16 -----
+    const int t = threadIdx.x - 256, c = t & (D / 16 - 1), r0 = t / (D / 16);
+    constexpr int RPS = 128 / (D / 16);                  // token rows of one sweep of the 128 threads
+    constexpr int NS = kPreKeys / RPS;                   // sweeps of a tile
+    const int32_t* table = a.table + (size_t)b * a.max_pages;
+    const int any_first = a.window > 0 ? max(rq.kv - rq.q + row0 / a.group + 1 - a.window, 0) : 0;
+    auto page_of = [&](int key) {
+      if (key >= rq.kv) return -2;
+      const int id = __ldg(table + (key >> a.page_log2));
+      return id >= 0 && id < a.num_pages ? id : -1;
+    };
+    // the 16 bytes that this thread converts in each sweep of tile j
+    auto load = [&](const uint8_t* codes, int j, uint4 (&x)[NS]) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const int key = j * kPreKeys + RPS * s + r0;
+        x[s] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+        const int p = page_of(key);
+        if (p >= 0)
+          x[s] = __ldg(reinterpret_cast<const uint4*>(
+              codes + ((((size_t)p * a.Hkv + h) << a.page_log2) + (size_t)(key & ((1 << a.page_log2) - 1))) * D + 16 * c));
+      }
+    };
+    // 16 codes are two 16-byte chunks of a row; the upper channels' threads store their second chunk first,
+    // so a quarter-warp's 8 stores fall on different banks
+    auto store = [&](uint8_t (*dst)[kPreKeys * 128], const uint4 (&x)[NS]) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const int r = RPS * s + r0;
+        uint4 lo4 = make_uint4(codes_lo(x[s].x), codes_hi(x[s].x), codes_lo(x[s].y), codes_hi(x[s].y));
+        uint4 hi4 = make_uint4(codes_lo(x[s].z), codes_hi(x[s].z), codes_lo(x[s].w), codes_hi(x[s].w));
+        const uint32_t base = tc::su32(&dst[c >> 2][r * 128]);
+        const int ch = (c & 3) * 2, flip = D == 128 ? (c >> 2) & 1 : r & 1;
+        const uint4 one = flip ? hi4 : lo4, two = flip ? lo4 : hi4;
+        sts128(base + (((ch + flip) ^ (r & 7)) << 4), one);
+        sts128(base + (((ch + 1 - flip) ^ (r & 7)) << 4), two);
+      }
+    };
+    // Scales of tile j: thread g < 8 of the first warp holds those of 16-key group g. The key scale of a group
+    // that no row sees is 1, and none is below the smallest that appending gives, so that a masked score
+    // (minus infinity) stays one when it is multiplied.
+    float ks = 1.f, vs = 0.f, vref = 0.f;
+    bool absent = false;
+    auto load_scales = [&](int j) {
+      ks = 1.f;
+      vs = 0.f;
+      absent = false;
+      if (t < kPreGroups) {
+        const int key = j * kPreKeys + 16 * t;
+        const int p = page_of(key);
+        if (p == -1) {
+          set_device_error(HBL_ERR_INVALID_ARG);
+          absent = true;
+        } else if (p >= 0 && key + 16 > any_first) {
+          ks = fmaxf(__ldg(a.kscale + (size_t)p * a.Hkv + h), kScaleFloor);
+          vs = __ldg(a.vscale + (size_t)p * a.Hkv + h);
+        }
+      }
+    };
+    uint4 kx[NS], vx[NS];
+    if (lo < hi) {
+      load(a.kcodes, lo, kx);
+      load_scales(lo);
+      load(a.vcodes, lo, vx);
+    }
+    for (int j = lo; j < hi; ++j) {
+      const int n = j - lo, st = n & 1;
+      const uint32_t ph = (uint32_t)(n >> 1) & 1u;
+      if (n >= 2 && !__all_sync(0xffffffffu, tc::mbar_wait(&S.k_empty[st], ph ^ 1u, abort))) break;
+      store(S.k[st], kx);
+      if (warp == 8) {
+        float vm = vs;
+#pragma unroll
+        for (int o = 1; o < kPreGroups; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+        vm = __shfl_sync(0xffffffffu, vm, 0);
+        const unsigned bad = __ballot_sync(0xffffffffu, absent);
+        if (vref == 0.f || vm > kPreSlack * vref) vref = vm;
+        if (t < kPreGroups) {
+          float* dst = S.scale[n % kPreRing];
+          const float lv = vs > 0.f ? fmaxf(log2f(__fdividef(vs, vref)), kPreLeast) : kPreLeast;
+          dst[t] = ks;
+          dst[8 + t] = lv;
+          dst[16 + t] = exp2f(-lv);
+          if (t == 0) {
+            dst[24] = vref;
+            dst[25] = __uint_as_float(bad);
+          }
+        }
+      }
+      fence_async_smem();
+      tc::mbar_arrive(&S.k_full[st]);
+      if (j + 1 < hi) {
+        load(a.kcodes, j + 1, kx);
+        load_scales(j + 1);
+      }
+      if (n >= 2 && !__all_sync(0xffffffffu, tc::mbar_wait(&S.v_empty[st], ph ^ 1u, abort))) break;
+      store(S.v[st], vx);
+      fence_async_smem();
+      tc::mbar_arrive(&S.v_full[st]);
+      if (j + 1 < hi) load(a.vcodes, j + 1, vx);
+    }
+  } else if (warp == 12 && lane == 0) {
+    // ----- tensor cores -----
+    const uint32_t id_s = idesc_f16(kPreKeys, false), id_o = idesc_f16(D, true);
+    bool ok = true;
+    auto scores = [&](int w, int st) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        mma_f16_ss(tmem + 128u * w, tc::smem_desc_sw128(tc::su32(&S.q[w][k >> 2][0]) + (k & 3) * 32),
+                   tc::smem_desc_sw128(tc::su32(&S.k[st][k >> 2][0]) + (k & 3) * 32), id_s, k > 0);
+      tc::tc_commit(&S.s_full[w]);
+    };
+    auto outputs = [&](int w, int st, bool first) {
+#pragma unroll
+      for (int k = 0; k < kPreKeys / 16; ++k)
+        mma_f16_ts(tmem + 256u + 128u * w, tmem + 128u * w + 8u * k,
+                   smem_desc_mn(tc::su32(&S.v[st][0][0]) + k * 2048, kPreKeys * 128), id_o, (!first || k > 0) ? 1u : 0u);
+    };
+    int done[2] = {0, 0};                              // tiles whose P V was issued, of each half
+    // step j: the outputs of tile j - 1, then the scores of tile j, for one half after the other
+    for (int j = lo; j <= hi && ok && lo < hi; ++j) {
+      const int n = j - lo, st = n & 1;
+      if (j < hi) {
+        ok = tc::mbar_wait(&S.k_full[st], (uint32_t)(n >> 1) & 1u, abort);
+        if (!ok) break;
+      }
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        if (j > lo && j - 1 >= half[w].lo && j - 1 < half[w].hi) {
+          ok = tc::mbar_wait(&S.p_full[w], (uint32_t)done[w] & 1u, abort) &&
+               tc::mbar_wait(&S.v_full[st ^ 1], (uint32_t)((n - 1) >> 1) & 1u, abort);
+          if (!ok) break;
+          tc::tc_fence_after();
+          outputs(w, st ^ 1, done[w] == 0);
+          if (++done[w] == half[w].hi - half[w].lo) tc::tc_commit(&S.o_full[w]);
+        }
+        if (j >= half[w].lo && j < half[w].hi) {
+          if (j == half[w].lo && !(ok = tc::mbar_wait(&S.q_full[w], 0, abort))) break;
+          tc::tc_fence_after();
+          scores(w, st);
+        }
+      }
+      if (j < hi) tc::tc_commit(&S.k_empty[st]);
+      if (j > lo) tc::tc_commit(&S.v_empty[st ^ 1]);
+    }
+    tc::tc_commit(&S.drained);
+    // outstanding products read shared memory: wait (bounded) until they are done
+    const long long t0 = clock64();
+    while (!tc::mbar_try_wait(&S.drained, 0) && clock64() - t0 < tc::kSpinLimit) {
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace kv
+}  // namespace hbl

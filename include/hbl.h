@@ -350,8 +350,12 @@ size_t hbl_kv_attention_workspace_bytes(int B, int D);
  *   cu_q    : device int32 B + 1, ascending: request b's rows are
  *             [cu_q[b], cu_q[b + 1]), its last ones the last of its cache.
  *   kv_lens : device int32 B: cached tokens, the new ones among them.
- *   max_q, max_kv : bounds of a request's rows and cached tokens that the
- *             caller knows (0: none); they choose kernels and never results.
+ *   max_q   : the most rows that a request has, as far as the caller knows (0:
+ *             T). It decides which kernels are launched; the rows of a request
+ *             with more are left as they were, which is recorded in the device
+ *             error word.
+ *   max_kv  : the most cached tokens likewise (0: max_pages * page). A hint:
+ *             it changes no result.
  *   scale   : finite, > 0; multiplies the scores.
  *   causal  : 1: row i of q sees the keys up to position kv - q + i; 0: all.
  *   window  : > 0 (with causal only): and of those the last `window`. 0: none.

@@ -273,6 +273,43 @@ def test_attention_prompts(L, Hq, Hkv, D, page, causal, window):
           window=window)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(2, 1, 128, 16), (2, 2, 64, 32), (3, 1, 64, 128)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 300)])
+def test_attention_long_prompts(L, Hq, Hkv, D, page, causal, window):
+    """More keys than any ring holds, more rows than a tile, block scales that keep outgrowing what came before."""
+    case = make_case(L, 15, [450, 130], [1500, 2049], Hq, Hkv, D, page, scale_spread=1.5)
+    check(L, case, causal=causal, window=window)
+    cache, Q, cu, kvs, table = case
+    grow = torch.arange(table.shape[1], device="cuda", dtype=torch.float32)
+    for b in range(2):                                       # louder from page to page, keys and values
+        at = torch.tensor(table[b], device="cuda").long()[:-(-int(kvs[b]) // page)]
+        cache.kscale[at] = (0.002 * 1.05 ** grow[:len(at)])[:, None].clamp(max=0.1)
+        cache.vscale[at] = (1e-6 * 1.5 ** grow[:len(at)])[:, None].clamp(max=1e3)
+    check(L, case, causal=causal, window=window)
+
+
+def test_attention_prompts_of_all_scales(L):
+    """Zero scales, and first tiles that a row does not see at all."""
+    case = make_case(L, 16, [300, 100], [300, 60], 2, 1, 128, 32)
+    check(L, case)
+    case[0].vscale[:] = 0
+    check(L, case)
+    case[0].vscale[::2] = 0.5
+    case[0].kscale[::3] = 0
+    check(L, case)
+
+
+def test_attention_rows_beyond_the_bound_are_left(L):
+    from hadamard_bit_quant_b200 import hbl
+    case = make_case(L, 17, [2, 300], [50, 400], 4, 2, 64, 16)
+    cache, Q, cu, kvs, table = case
+    out = torch.full_like(Q, 7.0)
+    cache.attention(Q, i32(cu), i32(kvs), i32(table), max_q=2, out=out)
+    assert hbl.hbl_get_device_error() == 1
+    assert bool((out[2:] == 7).all())
+    assert torch.equal(out[:2], cache.attention(Q, i32(cu), i32(kvs), i32(table))[:2])
+
+
 def test_attention_hints_do_not_change_results(L):
     case = make_case(L, 6, [1, 4, 150], [100, 900, 400], 8, 2, 128, 32)
     got = [check(L, case, **kw) if not kw else case[0].attention(case[1], i32(case[2]), i32(case[3]), i32(case[4]),
