@@ -6,6 +6,7 @@
 // request and streams the keys in tiles of 128:
 //   * warps 8..11 read the codes, turn them into fp16 exactly and store them 128B-swizzled (keys and
 //     values have the same layout: token rows of 64 channels; the keys are read K-major, the values MN-major);
+//   * warp 13 keeps the block scales a few tiles ahead;
 //   * warp 12 issues tcgen05.mma kind::f16: S = Q K^T into TMEM, then O += P V with P as the A operand from TMEM;
 //   * warps 0..3 and 4..7 (a thread for each of 128 rows, twice) turn S into P in place. While one half's
 //     softmax runs, the tensor cores work for the other half: S, P and O of both fill the 512 TMEM columns.
@@ -38,7 +39,7 @@ template <int D> struct __align__(1024) PreSmem {
   // of each tile: [0, 8) key scales of the 16-key groups, [8, 16) log2 of their value scales relative to the
   // reference, [16, 24) the inverses of those, [24] the reference, [25] bits of the groups that are not in the cache
   float scale[kPreRing][32];
-  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
+  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_full[2];
   uint64_t drained;
   long long sh[33];
   int item_b;
@@ -47,17 +48,30 @@ template <int D> struct __align__(1024) PreSmem {
   int abort;
 };
 
+// One lane of a converged warp issues; the operands stay warp-uniform, so they need no transfer to uniform
+// registers for each instruction.
 HBL_DEVINL void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accum)
+      "{\n.reg .pred p, e;\nsetp.ne.b32 p, %4, 0;\nelect.sync _|e, 0xffffffff;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accum)
       : "memory");
 }
 HBL_DEVINL void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accum)
+      "{\n.reg .pred p, e;\nsetp.ne.b32 p, %4, 0;\nelect.sync _|e, 0xffffffff;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accum)
       : "memory");
+}
+HBL_DEVINL void commit(uint64_t* bar) {
+  asm volatile(
+      "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(tc::su32(bar))
+      : "memory");
+}
+
+// tc::mbar_wait with the usual case, a phase that is over already, in front.
+HBL_DEVINL bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return tc::mbar_try_wait(bar, parity) || tc::mbar_wait(bar, parity, abort);
 }
 
 // Instruction descriptor: D fp32, A and B fp16, M = 128, N = n; bit 16: B is MN-major.
@@ -77,6 +91,27 @@ HBL_DEVINL uint64_t smem_desc_mn(uint32_t saddr, uint32_t lead) {
                "r"(r[14]), "r"(r[15])                                                                            \
                : "memory")
 
+HBL_DEVINL uint4 ldg_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+HBL_DEVINL float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// The block starts with 128 registers a thread; the softmax warps hold a row of 128 scores, so the others hand
+// theirs over: 2 x 168 + 112 + 64 for four warpgroups of 128 threads, the 512 of the launch.
+constexpr int kPreRegsSoftmax = 168, kPreRegsConvert = 112, kPreRegsRest = 64;
+static_assert(2 * kPreRegsSoftmax + kPreRegsConvert + kPreRegsRest <= 4 * 128, "registers of the launch");
+template <int N> HBL_DEVINL void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
+template <int N> HBL_DEVINL void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
+
 HBL_DEVINL void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
 HBL_DEVINL void sts128(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -92,6 +127,20 @@ HBL_DEVINL TileRange tiles_seen(const AttnArgs& a, const Request& rq, int row_a,
   if (last <= first) return {0, 0};
   return {first / kPreKeys, (last + kPreKeys - 1) / kPreKeys};
 }
+
+// Lane g (mod 8) looks up the page of the 16-key group g of a tile: -2 behind the last key, -1 where the page is not in
+// the cache. The tables are fetched a tile before the codes are, and looked at only then: a warp stops at the first use
+// of what it loads, and no load is to wait for another one.
+struct PageLookup {
+  int id = -2, raw = -2;
+  bool beyond = true;
+  HBL_DEVINL void fetch(const AttnArgs& a, const int32_t* table, int kv, int j, int lane) {
+    const int key = j * kPreKeys + 16 * (lane & 7);
+    beyond = key >= kv;
+    raw = beyond ? -2 : __ldg(table + (key >> a.page_log2));
+  }
+  HBL_DEVINL void settle(const AttnArgs& a) { id = beyond ? -2 : raw < 0 || raw >= a.num_pages ? -1 : raw; }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnArgs a) {
@@ -139,12 +188,13 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&S.q_full[i], 128);
-      tc::mbar_init(&S.k_full[i], 128);
+      tc::mbar_init(&S.k_full[i], 129);
       tc::mbar_init(&S.k_empty[i], 1);
       tc::mbar_init(&S.v_full[i], 128);
       tc::mbar_init(&S.v_empty[i], 1);
       tc::mbar_init(&S.s_full[i], 1);
-      tc::mbar_init(&S.p_full[i], 128);
+      tc::mbar_init(&S.p_full[i][0], 128);
+      tc::mbar_init(&S.p_full[i][1], 128);
       tc::mbar_init(&S.o_full[i], 1);
     }
     tc::mbar_init(&S.drained, 1);
@@ -182,6 +232,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
 
   if (warp < 8) {
     // ----- a row's softmax -----
+    regs_up<kPreRegsSoftmax>();
     const int w = warp >> 2;
     const int r = row0 + 128 * w + (threadIdx.x & 127);
     const bool live = r < nrows;
@@ -227,48 +278,36 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     bool ok = true;
     for (int j = half[w].lo; j < half[w].hi; ++j) {
       const int n = j - half[w].lo;
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(&S.s_full[w], (uint32_t)n & 1u, abort));
+      ok = __all_sync(0xffffffffu, wait(&S.s_full[w], (uint32_t)n & 1u, abort));
       if (!ok) break;
       tc::tc_fence_after();
       const uint32_t sc = tc::su32(&S.scale[(j - lo) % kPreRing][0]);
-      float f[kPreGroups], add[kPreGroups];
-#pragma unroll
-      for (int g = 0; g < kPreGroups; g += 4) {
-        const uint4 x = lds128(sc + 4 * g), y = lds128(sc + 32 + 4 * g);
-        f[g] = __uint_as_float(x.x); f[g + 1] = __uint_as_float(x.y);
-        f[g + 2] = __uint_as_float(x.z); f[g + 3] = __uint_as_float(x.w);
-        add[g] = __uint_as_float(y.x); add[g + 1] = __uint_as_float(y.y);
-        add[g + 2] = __uint_as_float(y.z); add[g + 3] = __uint_as_float(y.w);
-      }
       const float vnow = lds32f(sc + 96);
       const uint32_t bad = __float_as_uint(lds32f(sc + 100));
-#pragma unroll
-      for (int g = 0; g < kPreGroups; ++g) f[g] *= qs;
       const int key0 = j * kPreKeys;
       const bool whole = key0 >= lane_lo && key0 + kPreKeys <= lane_hi && bad == 0;
       // columns [c_lo, c_hi) are seen by this row
       const int c_lo = first - key0, c_hi = last - key0;
+      uint32_t x[kPreKeys];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) HBL_TMEM_LD32(s_addr + 32u * c, (x + 32 * c));
+      tc::tc_wait_ld();
+      if (!whole) {
+#pragma unroll
+        for (int i = 0; i < kPreKeys; ++i)
+          if (i < c_lo || i >= c_hi || (bad >> (i >> 4)) & 1) x[i] = 0xff800000u;
+      }
       float mt = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t x[32];
-        HBL_TMEM_LD32(s_addr + 32u * c, x);
-        tc::tc_wait_ld();
-        if (!whole) {
+      for (int g = 0; g < kPreGroups; ++g) {
+        float y[5];
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (32 * c + i < c_lo || 32 * c + i >= c_hi || (bad >> (2 * c + (i >> 4))) & 1) x[i] = 0xff800000u;
-          HBL_TMEM_ST32(s_addr + 32u * c, x);                // masked for the second reading too
-        }
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          float y = __uint_as_float(x[16 * g]);
-#pragma unroll
-          for (int i = 1; i < 16; ++i) y = fmaxf(y, __uint_as_float(x[16 * g + i]));
-          mt = fmaxf(mt, y * f[2 * c + g]);
-        }
+        for (int i = 0; i < 5; ++i)
+          y[i] = max3(__uint_as_float(x[16 * g + 3 * i]), __uint_as_float(x[16 * g + 3 * i + 1]),
+                      __uint_as_float(x[16 * g + 3 * i + 2]));
+        const float z = max3(max3(y[0], y[1], y[2]), max3(y[3], y[4], __uint_as_float(x[16 * g + 15])), -INFINITY);
+        mt = fmaxf(mt, z * (lds32f(sc + 4 * g) * qs));
       }
-      if (!whole) tc::tc_wait_st();
       const float mn = mt > m + kPreLag ? mt : m;
       const float alpha = mn == m ? 1.f : exp2_fast(m - mn);
       const float shrink = vref == vnow ? 1.f : __fdividef(vref, vnow);
@@ -291,32 +330,34 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       const float mu = m == -INFINITY ? 0.f : m;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        uint32_t x[32], p[16];
-        HBL_TMEM_LD32(s_addr + 32u * c, x);
-        tc::tc_wait_ld();
+        uint32_t p[16];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const float ff = f[2 * c + g], aa = add[2 * c + g] - mu;
-          float sum = 0.f;
+        for (int g = 2 * c; g < 2 * c + 2; ++g) {
+          const float fg = lds32f(sc + 4 * g) * qs, ag = lds32f(sc + 32 + 4 * g) - mu;
+          const float2 ff = make_float2(fg, fg), aa = make_float2(ag, ag);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float e = exp2_fast(__fmaf_rn(__uint_as_float(x[16 * g + i]), ff, aa));
-            sum += e;
-            x[16 * g + i] = __float_as_uint(e);
+          for (int i = 0; i < 8; ++i) {
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[16 * g + 2 * i]),
+                                                    __uint_as_float(x[16 * g + 2 * i + 1])), ff, aa);
+            const float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+            sum[i & 1] = __fadd2_rn(sum[i & 1], e);
+            p[8 * (g & 1) + i] = pack_half(e.x, e.y);
           }
-          l = __fmaf_rn(sum, lds32f(sc + 64 + 4 * (2 * c + g)), l);
+          const float2 t = __fadd2_rn(sum[0], sum[1]);
+          l = __fmaf_rn(t.x + t.y, lds32f(sc + 64 + 4 * g), l);
         }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) p[i] = pack_half(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
         HBL_TMEM_ST16(s_addr + 16u * c, p);
+        if (c & 1) {                                     // half of the keys: the product may begin
+          tc::tc_wait_st();
+          tc::tc_fence_before();
+          tc::mbar_arrive(&S.p_full[w][c >> 1]);
+        }
       }
-      tc::tc_wait_st();
-      tc::tc_fence_before();
-      tc::mbar_arrive(&S.p_full[w]);
     }
     // ----- the row's output -----
     const bool any = half[w].lo < half[w].hi;
-    if (any) ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(&S.o_full[w], 0, abort));
+    if (any) ok = ok && __all_sync(0xffffffffu, wait(&S.o_full[w], 0, abort));
     if (ok && !*abort) {
       tc::tc_fence_after();
       const bool some = l > 0.f || l != l;
@@ -348,154 +389,187 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     }
   } else if (warp < 12) {
     // ----- codes to fp16 -----
-    const int t = threadIdx.x - 256, c = t & (D / 16 - 1), r0 = t / (D / 16);
-    constexpr int RPS = 128 / (D / 16);                  // token rows of one sweep of the 128 threads
+    regs_down<kPreRegsConvert>();
+    // Thread t converts 16 codes of a row, the channels [16 q, 16 q + 16) of panel `pan`, in each of NS sweeps. The
+    // 8 threads of a store phase hold an even and an odd row, whose chunks 2 q ^ row fall on different banks.
+    const int t = threadIdx.x - 256, q = t & 3;
+    const int pan = D == 128 ? (t >> 3) & 1 : 0, r0 = D == 128 ? ((t >> 4) << 1) | ((t >> 2) & 1) : t >> 2;
+    constexpr int RPS = 128 * 64 / (D * 4);              // token rows of one sweep of the 128 threads
     constexpr int NS = kPreKeys / RPS;                   // sweeps of a tile
     const int32_t* table = a.table + (size_t)b * a.max_pages;
-    const int any_first = a.window > 0 ? max(rq.kv - rq.q + row0 / a.group + 1 - a.window, 0) : 0;
-    auto page_of = [&](int key) {
-      if (key >= rq.kv) return -2;
-      const int id = __ldg(table + (key >> a.page_log2));
-      return id >= 0 && id < a.num_pages ? id : -1;
-    };
-    // the 16 bytes that this thread converts in each sweep of tile j
-    auto load = [&](const uint8_t* codes, int j, uint4 (&x)[NS]) {
+    const uint32_t pmask = (1u << a.page_log2) - 1u;
+    const size_t block = (size_t)D << a.page_log2;       // bytes of a page's head
+    const size_t mine = h * block + (size_t)(r0 & pmask) * D + (size_t)(64 * pan + 16 * q);
+    const uint8_t* kbase = a.kcodes + mine;
+    const uint8_t* vbase = a.vcodes + mine;
+    const uint32_t step = (uint32_t)(a.Hkv * block), pbytes = pmask * D;
+    PageLookup look;
+    // Keys that no row sees are fetched too, from some page: their codes are finite, and they count for nothing.
+    auto load = [&](const uint8_t* base, uint4 (&x)[NS]) {
+      uint32_t pb = pbytes;
+      asm volatile("" : "+r"(pb));                       // the sweeps' addresses are not to be kept in registers
+      const int known = max(look.id, 0);
+      int id[NS];
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        const int key = j * kPreKeys + RPS * s + r0;
-        x[s] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-        const int p = page_of(key);
-        if (p >= 0)
-          x[s] = __ldg(reinterpret_cast<const uint4*>(
-              codes + ((((size_t)p * a.Hkv + h) << a.page_log2) + (size_t)(key & ((1 << a.page_log2) - 1))) * D + 16 * c));
-      }
+      for (int s = 0; s < NS; ++s) id[s] = __shfl_sync(0xffffffffu, known, RPS * s / 16 + (RPS > 16 ? r0 >> 4 : 0));
+#pragma unroll
+      for (int s = 0; s < NS; ++s) x[s] = ldg_stream(base + (uint64_t)(uint32_t)id[s] * step + ((RPS * s * D) & pb));
     };
-    // 16 codes are two 16-byte chunks of a row; the upper channels' threads store their second chunk first,
-    // so a quarter-warp's 8 stores fall on different banks
+    const uint32_t to = (uint32_t)(pan * kPreKeys * 128 + r0 * 128);
+    const uint32_t c0 = to + (((2 * q) ^ (r0 & 7)) << 4), c1 = to + (((2 * q + 1) ^ (r0 & 7)) << 4);
     auto store = [&](uint8_t (*dst)[kPreKeys * 128], const uint4 (&x)[NS]) {
+      const uint32_t base = tc::su32(&dst[0][0]);
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        const int r = RPS * s + r0;
-        uint4 lo4 = make_uint4(codes_lo(x[s].x), codes_hi(x[s].x), codes_lo(x[s].y), codes_hi(x[s].y));
-        uint4 hi4 = make_uint4(codes_lo(x[s].z), codes_hi(x[s].z), codes_lo(x[s].w), codes_hi(x[s].w));
-        const uint32_t base = tc::su32(&dst[c >> 2][r * 128]);
-        const int ch = (c & 3) * 2, flip = D == 128 ? (c >> 2) & 1 : r & 1;
-        const uint4 one = flip ? hi4 : lo4, two = flip ? lo4 : hi4;
-        sts128(base + (((ch + flip) ^ (r & 7)) << 4), one);
-        sts128(base + (((ch + 1 - flip) ^ (r & 7)) << 4), two);
-      }
-    };
-    // Scales of tile j: thread g < 8 of the first warp holds those of 16-key group g. The key scale of a group
-    // that no row sees is 1, and none is below the smallest that appending gives, so that a masked score
-    // (minus infinity) stays one when it is multiplied.
-    float ks = 1.f, vs = 0.f, vref = 0.f;
-    bool absent = false;
-    auto load_scales = [&](int j) {
-      ks = 1.f;
-      vs = 0.f;
-      absent = false;
-      if (t < kPreGroups) {
-        const int key = j * kPreKeys + 16 * t;
-        const int p = page_of(key);
-        if (p == -1) {
-          set_device_error(HBL_ERR_INVALID_ARG);
-          absent = true;
-        } else if (p >= 0 && key + 16 > any_first) {
-          ks = fmaxf(__ldg(a.kscale + (size_t)p * a.Hkv + h), kScaleFloor);
-          vs = __ldg(a.vscale + (size_t)p * a.Hkv + h);
-        }
+        sts128(base + c0 + RPS * 128 * s, make_uint4(codes_lo(x[s].x), codes_hi(x[s].x), codes_lo(x[s].y), codes_hi(x[s].y)));
+        sts128(base + c1 + RPS * 128 * s, make_uint4(codes_lo(x[s].z), codes_hi(x[s].z), codes_lo(x[s].w), codes_hi(x[s].w)));
       }
     };
     uint4 kx[NS], vx[NS];
     if (lo < hi) {
-      load(a.kcodes, lo, kx);
-      load_scales(lo);
-      load(a.vcodes, lo, vx);
+      look.fetch(a, table, rq.kv, lo, lane);
+      look.settle(a);
+      load(kbase, kx);
+      load(vbase, vx);
+      if (lo + 1 < hi) look.fetch(a, table, rq.kv, lo + 1, lane);
     }
     for (int j = lo; j < hi; ++j) {
       const int n = j - lo, st = n & 1;
       const uint32_t ph = (uint32_t)(n >> 1) & 1u;
-      if (n >= 2 && !__all_sync(0xffffffffu, tc::mbar_wait(&S.k_empty[st], ph ^ 1u, abort))) break;
+      if (n >= 2 && !__all_sync(0xffffffffu, wait(&S.k_empty[st], ph ^ 1u, abort))) break;
       store(S.k[st], kx);
-      if (warp == 8) {
-        float vm = vs;
-#pragma unroll
-        for (int o = 1; o < kPreGroups; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
-        vm = __shfl_sync(0xffffffffu, vm, 0);
-        const unsigned bad = __ballot_sync(0xffffffffu, absent);
-        if (vref == 0.f || vm > kPreSlack * vref) vref = vm;
-        if (t < kPreGroups) {
-          float* dst = S.scale[n % kPreRing];
-          const float lv = vs > 0.f ? fmaxf(log2f(__fdividef(vs, vref)), kPreLeast) : kPreLeast;
-          dst[t] = ks;
-          dst[8 + t] = lv;
-          dst[16 + t] = exp2f(-lv);
-          if (t == 0) {
-            dst[24] = vref;
-            dst[25] = __uint_as_float(bad);
-          }
-        }
-      }
       fence_async_smem();
       tc::mbar_arrive(&S.k_full[st]);
       if (j + 1 < hi) {
-        load(a.kcodes, j + 1, kx);
-        load_scales(j + 1);
+        look.settle(a);
+        load(kbase, kx);
       }
-      if (n >= 2 && !__all_sync(0xffffffffu, tc::mbar_wait(&S.v_empty[st], ph ^ 1u, abort))) break;
+      if (n >= 2 && !__all_sync(0xffffffffu, wait(&S.v_empty[st], ph ^ 1u, abort))) break;
       store(S.v[st], vx);
       fence_async_smem();
       tc::mbar_arrive(&S.v_full[st]);
-      if (j + 1 < hi) load(a.vcodes, j + 1, vx);
+      if (j + 1 < hi) {
+        load(vbase, vx);
+        if (j + 2 < hi) look.fetch(a, table, rq.kv, j + 2, lane);
+      }
     }
-  } else if (warp == 12 && lane == 0) {
+  } else {
     // ----- tensor cores -----
-    const uint32_t id_s = idesc_f16(kPreKeys, false), id_o = idesc_f16(D, true);
-    bool ok = true;
-    auto scores = [&](int w, int st) {
+    regs_down<kPreRegsRest>();
+    if (warp == 12) {
+      const uint32_t id_s = idesc_f16(kPreKeys, false), id_o = idesc_f16(D, true);
+      bool ok = true;
+      auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
+      // descriptors of the first step; a step on is an addition to the address field (16-byte units)
+      const uint64_t q_d = tc::smem_desc_sw128(tc::su32(&S.q[0][0][0])), k_d = tc::smem_desc_sw128(tc::su32(&S.k[0][0][0]));
+      const uint64_t v_d = smem_desc_mn(tc::su32(&S.v[0][0][0]), kPreKeys * 128);
+      constexpr int kTileUnits = D / 64 * kPreKeys * 128 / 16;      // a tile of Q, K or V
+      auto scores = [&](int w, int st) {
+        const uint64_t qd = q_d + w * kTileUnits, kd = k_d + st * kTileUnits;
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        mma_f16_ss(tmem + 128u * w, tc::smem_desc_sw128(tc::su32(&S.q[w][k >> 2][0]) + (k & 3) * 32),
-                   tc::smem_desc_sw128(tc::su32(&S.k[st][k >> 2][0]) + (k & 3) * 32), id_s, k > 0);
-      tc::tc_commit(&S.s_full[w]);
-    };
-    auto outputs = [&](int w, int st, bool first) {
+        for (int k = 0; k < D / 16; ++k) {
+          const int at = (k >> 2) * (kPreKeys * 128 / 16) + (k & 3) * 2;
+          mma_f16_ss(tmem + 128u * w, qd + at, kd + at, id_s, k > 0);
+        }
+        commit(&S.s_full[w]);
+      };
+      auto outputs = [&](int w, int st, bool first, int part) {
+        const uint64_t vd = v_d + st * kTileUnits;
 #pragma unroll
-      for (int k = 0; k < kPreKeys / 16; ++k)
-        mma_f16_ts(tmem + 256u + 128u * w, tmem + 128u * w + 8u * k,
-                   smem_desc_mn(tc::su32(&S.v[st][0][0]) + k * 2048, kPreKeys * 128), id_o, (!first || k > 0) ? 1u : 0u);
-    };
-    int done[2] = {0, 0};                              // tiles whose P V was issued, of each half
-    // step j: the outputs of tile j - 1, then the scores of tile j, for one half after the other
-    for (int j = lo; j <= hi && ok && lo < hi; ++j) {
-      const int n = j - lo, st = n & 1;
-      if (j < hi) {
-        ok = tc::mbar_wait(&S.k_full[st], (uint32_t)(n >> 1) & 1u, abort);
-        if (!ok) break;
-      }
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        if (j > lo && j - 1 >= half[w].lo && j - 1 < half[w].hi) {
-          ok = tc::mbar_wait(&S.p_full[w], (uint32_t)done[w] & 1u, abort) &&
-               tc::mbar_wait(&S.v_full[st ^ 1], (uint32_t)((n - 1) >> 1) & 1u, abort);
+        for (int k = part * (kPreKeys / 32); k < (part + 1) * (kPreKeys / 32); ++k)
+          mma_f16_ts(tmem + 256u + 128u * w, tmem + 128u * w + 8u * k, vd + k * (2048 / 16), id_o,
+                     (!first || k > 0) ? 1u : 0u);
+      };
+      int done[2] = {0, 0};                              // tiles whose P V was issued, of each half
+      // step j: the outputs of tile j - 1, then the scores of tile j, for one half after the other
+      for (int j = lo; j <= hi && lo < hi; ++j) {
+        const int n = j - lo, st = n & 1;
+        if (j < hi) {
+          ok = all(wait(&S.k_full[st], (uint32_t)(n >> 1) & 1u, abort));
           if (!ok) break;
-          tc::tc_fence_after();
-          outputs(w, st ^ 1, done[w] == 0);
-          if (++done[w] == half[w].hi - half[w].lo) tc::tc_commit(&S.o_full[w]);
         }
-        if (j >= half[w].lo && j < half[w].hi) {
-          if (j == half[w].lo && !(ok = tc::mbar_wait(&S.q_full[w], 0, abort))) break;
-          tc::tc_fence_after();
-          scores(w, st);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (j > lo && j - 1 >= half[w].lo && j - 1 < half[w].hi) {
+            ok = all(wait(&S.v_full[st ^ 1], (uint32_t)((n - 1) >> 1) & 1u, abort));
+#pragma unroll
+            for (int part = 0; part < 2 && ok; ++part) {
+              ok = all(wait(&S.p_full[w][part], (uint32_t)done[w] & 1u, abort));
+              if (!ok) break;
+              tc::tc_fence_after();
+              outputs(w, st ^ 1, done[w] == 0, part);
+            }
+            if (!ok) break;
+            if (++done[w] == half[w].hi - half[w].lo) commit(&S.o_full[w]);
+          }
+          if (j >= half[w].lo && j < half[w].hi) {
+            if (j == half[w].lo && !(ok = all(wait(&S.q_full[w], 0, abort)))) break;
+            tc::tc_fence_after();
+            scores(w, st);
+          }
+        }
+        if (!ok) break;
+        if (j < hi) commit(&S.k_empty[st]);
+        if (j > lo) commit(&S.v_empty[st ^ 1]);
+      }
+      commit(&S.drained);
+      // outstanding products read shared memory: wait (bounded) until they are done
+      const long long t0 = clock64();
+      while (!tc::mbar_try_wait(&S.drained, 0) && clock64() - t0 < tc::kSpinLimit) {
+      }
+    } else if (warp == 13) {
+      // ----- block scales -----
+      // Lane g < 8 holds those of group g. The key scale of a group that no row sees is 1, and none is below the
+      // smallest that appending gives, so that a masked score (minus infinity) stays one when it is multiplied.
+      const int32_t* table = a.table + (size_t)b * a.max_pages;
+      const int any_first = a.window > 0 ? max(rq.kv - rq.q + row0 / a.group + 1 - a.window, 0) : 0;
+      float ks = 1.f, vs = 0.f, vref = 0.f;
+      bool absent = false;
+      PageLookup look;
+      auto load = [&](int j) {
+        look.settle(a);
+        ks = 1.f;
+        vs = 0.f;
+        absent = look.id == -1;
+        if (look.id >= 0 && j * kPreKeys + 16 * (lane & 7) + 16 > any_first) {
+          ks = __ldg(a.kscale + (size_t)look.id * a.Hkv + h);
+          vs = __ldg(a.vscale + (size_t)look.id * a.Hkv + h);
+        }
+      };
+      if (lo < hi) {
+        look.fetch(a, table, rq.kv, lo, lane);
+        load(lo);
+        if (lo + 1 < hi) look.fetch(a, table, rq.kv, lo + 1, lane);
+      }
+      for (int j = lo; j < hi; ++j) {
+        const int n = j - lo, st = n & 1;
+        float vm = vs;
+#pragma unroll
+        for (int o = 1; o < kPreGroups; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+        const unsigned bad = __ballot_sync(0xffffffffu, absent) & 0xffu;
+        if (vref == 0.f || vm > kPreSlack * vref) vref = vm;
+        const float lv = vs > 0.f ? fmaxf(__log2f(__fdividef(vs, vref)), kPreLeast) : kPreLeast;
+        // the ring's place is free: k_full of tile n - 1 was signalled behind the scores of tile n - 3, which wait for
+        // the probabilities of tile n - 4, its last user
+        if (lane < kPreGroups) {
+          float* dst = S.scale[n % kPreRing];
+          dst[lane] = fmaxf(ks, kScaleFloor);
+          dst[8 + lane] = lv;
+          dst[16 + lane] = exp2_fast(-lv);
+          if (lane == 0) {
+            dst[24] = vref;
+            dst[25] = __uint_as_float(bad);
+            if (bad) set_device_error(HBL_ERR_INVALID_ARG);
+          }
+        }
+        if (n >= 2 && !__all_sync(0xffffffffu, wait(&S.k_empty[st], ((uint32_t)(n >> 1) & 1u) ^ 1u, abort))) break;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&S.k_full[st]);
+        if (j + 1 < hi) {
+          load(j + 1);
+          if (j + 2 < hi) look.fetch(a, table, rq.kv, j + 2, lane);
         }
       }
-      if (j < hi) tc::tc_commit(&S.k_empty[st]);
-      if (j > lo) tc::tc_commit(&S.v_empty[st ^ 1]);
-    }
-    tc::tc_commit(&S.drained);
-    // outstanding products read shared memory: wait (bounded) until they are done
-    const long long t0 = clock64();
-    while (!tc::mbar_try_wait(&S.drained, 0) && clock64() - t0 < tc::kSpinLimit) {
     }
   }
   tc::tc_fence_before();
