@@ -7,7 +7,8 @@
 //   * warps 8..11 read the codes, turn them into fp16 exactly and store them 128B-swizzled (keys and
 //     values have the same layout: token rows of 64 channels; the keys are read K-major, the values MN-major);
 //   * warp 13 keeps the block scales a few tiles ahead;
-//   * warp 12 issues tcgen05.mma kind::f16: S = Q K^T into TMEM, then O += P V with P as the A operand from TMEM;
+//   * warps 12 and 14, one for each half of the rows, issue tcgen05.mma kind::f16: S = Q K^T into TMEM, 64 keys a
+//     step, then O += P V with P as the A operand from TMEM;
 //   * warps 0..3 and 4..7 (a thread for each of 128 rows, twice) turn S into P in place. While one half's
 //     softmax runs, the tensor cores work for the other half: S, P and O of both fill the 512 TMEM columns.
 // A row's reference maximum is raised only when the running one has outgrown it by 2^8, and the values' reference
@@ -24,8 +25,10 @@ namespace kv {
 
 constexpr int kPreRows = 256;            // query rows of a CTA, in two halves of 128
 constexpr int kPreKeys = 128;            // keys of a tile
+constexpr int kPreStep = 64;             // keys of a step: scores of two steps are held for each half
 constexpr int kPreThreads = 512;
 constexpr int kPreGroups = kPreKeys / 16;
+constexpr int kPreStepGroups = kPreStep / 16;
 constexpr int kPreRing = 4;              // tiles whose scales are held
 constexpr float kPreLag = 8.f;           // log2 of how far the running maximum may outgrow its reference
 constexpr float kPreSlack = 16.f;        // the same for the values' reference scale
@@ -39,8 +42,8 @@ template <int D> struct __align__(1024) PreSmem {
   // of each tile: [0, 8) key scales of the 16-key groups, [8, 16) log2 of their value scales relative to the
   // reference, [16, 24) the inverses of those, [24] the reference, [25] bits of the groups that are not in the cache
   float scale[kPreRing][32];
-  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_full[2];
-  uint64_t drained;
+  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2], p_full[2][2], o_full[2];
+  uint64_t drained[2];
   long long sh[33];
   int item_b;
   int item_off;
@@ -84,6 +87,15 @@ HBL_DEVINL uint64_t smem_desc_mn(uint32_t saddr, uint32_t lead) {
   return (tc::smem_desc_sw128(saddr) & ~((uint64_t)0x3fff << 16)) | ((uint64_t)(lead >> 4) << 16);
 }
 
+#define HBL_TMEM_LD16(addr, r)                                                                                   \
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}," \
+               " [%16];\n"                                                                                       \
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), \
+                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),        \
+                 "=r"(r[15])                                                                                     \
+               : "r"(addr)                                                                                       \
+               : "memory")
+
 #define HBL_TMEM_ST16(addr, r)                                                                                   \
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"   \
                "%15,%16};\n" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),      \
@@ -105,9 +117,9 @@ HBL_DEVINL float max3(float a, float b, float c) {
   return d;
 }
 
-// The block starts with 128 registers a thread; the softmax warps hold a row of 128 scores, so the others hand
-// theirs over: 2 x 168 + 112 + 64 for four warpgroups of 128 threads, the 512 of the launch.
-constexpr int kPreRegsSoftmax = 168, kPreRegsConvert = 112, kPreRegsRest = 64;
+// The block starts with 128 registers a thread; the converting warps hold 64 bytes in flight for each of keys and
+// values, so the others hand theirs over: 2 x 120 + 152 + 112 for four warpgroups of 128 threads.
+constexpr int kPreRegsSoftmax = 120, kPreRegsConvert = 152, kPreRegsRest = 112;
 static_assert(2 * kPreRegsSoftmax + kPreRegsConvert + kPreRegsRest <= 4 * 128, "registers of the launch");
 template <int N> HBL_DEVINL void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
 template <int N> HBL_DEVINL void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
@@ -189,15 +201,16 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&S.q_full[i], 128);
       tc::mbar_init(&S.k_full[i], 129);
-      tc::mbar_init(&S.k_empty[i], 1);
+      tc::mbar_init(&S.k_empty[i], 2);
       tc::mbar_init(&S.v_full[i], 128);
-      tc::mbar_init(&S.v_empty[i], 1);
-      tc::mbar_init(&S.s_full[i], 1);
+      tc::mbar_init(&S.v_empty[i], 2);
+      tc::mbar_init(&S.s_full[i][0], 1);
+      tc::mbar_init(&S.s_full[i][1], 1);
       tc::mbar_init(&S.p_full[i][0], 128);
       tc::mbar_init(&S.p_full[i][1], 128);
       tc::mbar_init(&S.o_full[i], 1);
+      tc::mbar_init(&S.drained[i], 1);
     }
-    tc::mbar_init(&S.drained, 1);
     S.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
@@ -232,7 +245,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
 
   if (warp < 8) {
     // ----- a row's softmax -----
-    regs_up<kPreRegsSoftmax>();
+    regs_down<kPreRegsSoftmax>();
     const int w = warp >> 2;
     const int r = row0 + 128 * w + (threadIdx.x & 127);
     const bool live = r < nrows;
@@ -245,7 +258,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       // the row in fp16, brought into its range by a power of two, to shared memory
       const uint4* src = reinterpret_cast<const uint4*>(a.Q + (size_t)(rq.row0 + tok) * (size_t)a.q_stride + (size_t)head * D);
       float amax = 0.f;
-#pragma unroll
+#pragma unroll 4
       for (int c = 0; c < D / 8; ++c) {
         const uint4 x = __ldg(src + c);
         const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
@@ -257,7 +270,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       row_power(amax, &up, &qs);
       qs *= a.scale_log2;
       const int rr = threadIdx.x & 127;
-#pragma unroll
+#pragma unroll 4
       for (int c = 0; c < D / 8; ++c) {
         const uint4 x = __ldg(src + c);
         const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
@@ -276,37 +289,42 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     const int lane_lo = __reduce_max_sync(0xffffffffu, first), lane_hi = __reduce_min_sync(0xffffffffu, last);
     float m = -INFINITY, l = 0.f, vref = 0.f;
     bool ok = true;
-    for (int j = half[w].lo; j < half[w].hi; ++j) {
-      const int n = j - half[w].lo;
-      ok = __all_sync(0xffffffffu, wait(&S.s_full[w], (uint32_t)n & 1u, abort));
+    const int steps = 2 * (half[w].hi - half[w].lo);
+    for (int n = 0; n < steps; ++n) {
+      ok = __all_sync(0xffffffffu, wait(&S.s_full[w][n & 1], (uint32_t)(n >> 1) & 1u, abort));
       if (!ok) break;
       tc::tc_fence_after();
-      const uint32_t sc = tc::su32(&S.scale[(j - lo) % kPreRing][0]);
-      const float vnow = lds32f(sc + 96);
-      const uint32_t bad = __float_as_uint(lds32f(sc + 100));
-      const int key0 = j * kPreKeys;
-      const bool whole = key0 >= lane_lo && key0 + kPreKeys <= lane_hi && bad == 0;
-      // columns [c_lo, c_hi) are seen by this row
-      const int c_lo = first - key0, c_hi = last - key0;
-      uint32_t x[kPreKeys];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) HBL_TMEM_LD32(s_addr + 32u * c, (x + 32 * c));
+      const int j = half[w].lo + (n >> 1), key0 = j * kPreKeys + kPreStep * (n & 1);
+      const uint32_t src = s_addr + (uint32_t)(kPreStep * (n & 1));
+      uint32_t x[kPreStep];
+      HBL_TMEM_LD32(src, x);
+      HBL_TMEM_LD32(src + 32u, (x + 32));
+      const uint32_t sc = tc::su32(&S.scale[(j - lo) % kPreRing][0]) + 16u * (n & 1);
+      const uint4 kq = lds128(sc), vq = lds128(sc + 32), iq = lds128(sc + 64);
+      const uint32_t sc0 = tc::su32(&S.scale[(j - lo) % kPreRing][0]);
+      const float vnow = lds32f(sc0 + 96);
+      const uint32_t bad = (__float_as_uint(lds32f(sc0 + 100)) >> (kPreStepGroups * (n & 1))) & 15u;
+      const float f[4] = {__uint_as_float(kq.x) * qs, __uint_as_float(kq.y) * qs, __uint_as_float(kq.z) * qs,
+                          __uint_as_float(kq.w) * qs};
+      const float add[4] = {__uint_as_float(vq.x), __uint_as_float(vq.y), __uint_as_float(vq.z), __uint_as_float(vq.w)};
+      const float back[4] = {__uint_as_float(iq.x), __uint_as_float(iq.y), __uint_as_float(iq.z), __uint_as_float(iq.w)};
       tc::tc_wait_ld();
-      if (!whole) {
+      if (!(key0 >= lane_lo && key0 + kPreStep <= lane_hi && bad == 0)) {
+        const int c_lo = first - key0, c_hi = last - key0;      // the columns that this row sees
 #pragma unroll
-        for (int i = 0; i < kPreKeys; ++i)
+        for (int i = 0; i < kPreStep; ++i)
           if (i < c_lo || i >= c_hi || (bad >> (i >> 4)) & 1) x[i] = 0xff800000u;
       }
       float mt = -INFINITY;
 #pragma unroll
-      for (int g = 0; g < kPreGroups; ++g) {
+      for (int g = 0; g < kPreStepGroups; ++g) {
         float y[5];
 #pragma unroll
         for (int i = 0; i < 5; ++i)
           y[i] = max3(__uint_as_float(x[16 * g + 3 * i]), __uint_as_float(x[16 * g + 3 * i + 1]),
                       __uint_as_float(x[16 * g + 3 * i + 2]));
-        const float z = max3(max3(y[0], y[1], y[2]), max3(y[3], y[4], __uint_as_float(x[16 * g + 15])), -INFINITY);
-        mt = fmaxf(mt, z * (lds32f(sc + 4 * g) * qs));
+        const float z = fmaxf(max3(y[0], y[1], y[2]), max3(y[3], y[4], __uint_as_float(x[16 * g + 15])));
+        mt = fmaxf(mt, z * f[g]);
       }
       const float mn = mt > m + kPreLag ? mt : m;
       const float alpha = mn == m ? 1.f : exp2_fast(m - mn);
@@ -316,25 +334,28 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       l *= alpha;
       const float ao = alpha * shrink;
       if (n > 0 && __any_sync(0xffffffffu, ao != 1.f)) {
-        // the products so far are complete: the scores of this tile were issued behind them
+        // Once the products so far are complete: the one before the last is, this step's scores came behind it.
+        ok = __all_sync(0xffffffffu, wait(&S.o_full[w], (uint32_t)(n - 1) & 1u, abort));
+        if (!ok) break;
+        tc::tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t x[32];
-          HBL_TMEM_LD32(o_addr + 32u * c, x);
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t o[16];
+          HBL_TMEM_LD16(o_addr + 16u * c, o);
           tc::tc_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * ao);
-          HBL_TMEM_ST32(o_addr + 32u * c, x);
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * ao);
+          HBL_TMEM_ST16(o_addr + 16u * c, o);
         }
       }
       const float mu = m == -INFINITY ? 0.f : m;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2; ++c) {
         uint32_t p[16];
 #pragma unroll
         for (int g = 2 * c; g < 2 * c + 2; ++g) {
-          const float fg = lds32f(sc + 4 * g) * qs, ag = lds32f(sc + 32 + 4 * g) - mu;
-          const float2 ff = make_float2(fg, fg), aa = make_float2(ag, ag);
+          const float ag = add[g] - mu;
+          const float2 ff = make_float2(f[g], f[g]), aa = make_float2(ag, ag);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -345,19 +366,19 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
             p[8 * (g & 1) + i] = pack_half(e.x, e.y);
           }
           const float2 t = __fadd2_rn(sum[0], sum[1]);
-          l = __fmaf_rn(t.x + t.y, lds32f(sc + 64 + 4 * g), l);
+          l = __fmaf_rn(t.x + t.y, back[g], l);
         }
-        HBL_TMEM_ST16(s_addr + 16u * c, p);
-        if (c & 1) {                                     // half of the keys: the product may begin
-          tc::tc_wait_st();
-          tc::tc_fence_before();
-          tc::mbar_arrive(&S.p_full[w][c >> 1]);
-        }
+        HBL_TMEM_ST16(src + 16u * c, p);
       }
+      tc::tc_wait_st();
+      tc::tc_fence_before();
+      tc::mbar_arrive(&S.p_full[w][n & 1]);
     }
     // ----- the row's output -----
-    const bool any = half[w].lo < half[w].hi;
-    if (any) ok = ok && __all_sync(0xffffffffu, wait(&S.o_full[w], 0, abort));
+    const bool any = steps > 0;
+    // all products but the last two are complete, so the two phases are told apart in turn
+    if (any) ok = ok && __all_sync(0xffffffffu, wait(&S.o_full[w], (uint32_t)steps & 1u, abort) &&
+                                                    wait(&S.o_full[w], (uint32_t)(steps - 1) & 1u, abort));
     if (ok && !*abort) {
       tc::tc_fence_after();
       const bool some = l > 0.f || l != l;
@@ -389,7 +410,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     }
   } else if (warp < 12) {
     // ----- codes to fp16 -----
-    regs_down<kPreRegsConvert>();
+    regs_up<kPreRegsConvert>();
     // Thread t converts 16 codes of a row, the channels [16 q, 16 q + 16) of panel `pan`, in each of NS sweeps. The
     // 8 threads of a store phase hold an even and an odd row, whose chunks 2 q ^ row fall on different banks.
     const int t = threadIdx.x - 256, q = t & 3;
@@ -456,66 +477,78 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
   } else {
     // ----- tensor cores -----
     regs_down<kPreRegsRest>();
-    if (warp == 12) {
-      const uint32_t id_s = idesc_f16(kPreKeys, false), id_o = idesc_f16(D, true);
-      bool ok = true;
-      auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
-      // descriptors of the first step; a step on is an addition to the address field (16-byte units)
-      const uint64_t q_d = tc::smem_desc_sw128(tc::su32(&S.q[0][0][0])), k_d = tc::smem_desc_sw128(tc::su32(&S.k[0][0][0]));
+    if (warp == 12 || warp == 14) {
+      const int w = (warp - 12) >> 1;
+      const TileRange mine = w ? half[1] : half[0];
+      const uint32_t id_s = idesc_f16(kPreStep, false), id_o = idesc_f16(D, true);
+      constexpr int kTileUnits = D / 64 * kPreKeys * 128 / 16;      // descriptors count in 16 bytes: a tile of Q, K or V
+      constexpr int kStepUnits = kPreStep * 128 / 16;               // the second step's rows in a panel
+      const uint64_t q_d = tc::smem_desc_sw128(tc::su32(&S.q[w][0][0])), k_d = tc::smem_desc_sw128(tc::su32(&S.k[0][0][0]));
       const uint64_t v_d = smem_desc_mn(tc::su32(&S.v[0][0][0]), kPreKeys * 128);
-      constexpr int kTileUnits = D / 64 * kPreKeys * 128 / 16;      // a tile of Q, K or V
-      auto scores = [&](int w, int st) {
-        const uint64_t qd = q_d + w * kTileUnits, kd = k_d + st * kTileUnits;
+      const uint32_t s_t = tmem + 128u * w, o_t = tmem + 256u + 128u * w;
+      auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
+      // tile t of the CTA: its stage and the phase of its barriers
+      auto full = [&](uint64_t* bar, int t) { return all(wait(bar + (t & 1), (uint32_t)(t >> 1) & 1u, abort)); };
+      auto scores = [&](int t, int part) {
+        const uint64_t kd = k_d + (t & 1) * kTileUnits + part * kStepUnits;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const int at = (k >> 2) * (kPreKeys * 128 / 16) + (k & 3) * 2;
-          mma_f16_ss(tmem + 128u * w, qd + at, kd + at, id_s, k > 0);
+          mma_f16_ss(s_t + kPreStep * part, q_d + at, kd + at, id_s, k > 0);
         }
-        commit(&S.s_full[w]);
+        commit(&S.s_full[w][part]);
       };
-      auto outputs = [&](int w, int st, bool first, int part) {
-        const uint64_t vd = v_d + st * kTileUnits;
+      auto outputs = [&](int t, int part, bool first) {
+        const uint64_t vd = v_d + (t & 1) * kTileUnits + part * kStepUnits;
 #pragma unroll
-        for (int k = part * (kPreKeys / 32); k < (part + 1) * (kPreKeys / 32); ++k)
-          mma_f16_ts(tmem + 256u + 128u * w, tmem + 128u * w + 8u * k, vd + k * (2048 / 16), id_o,
-                     (!first || k > 0) ? 1u : 0u);
+        for (int k = 0; k < kPreStep / 16; ++k)
+          mma_f16_ts(o_t, s_t + kPreStep * part + 8u * k, vd + k * (2048 / 16), id_o, (!first || k > 0) ? 1u : 0u);
+        commit(&S.o_full[w]);
       };
-      int done[2] = {0, 0};                              // tiles whose P V was issued, of each half
-      // step j: the outputs of tile j - 1, then the scores of tile j, for one half after the other
-      for (int j = lo; j <= hi && lo < hi; ++j) {
-        const int n = j - lo, st = n & 1;
-        if (j < hi) {
-          ok = all(wait(&S.k_full[st], (uint32_t)(n >> 1) & 1u, abort));
-          if (!ok) break;
-        }
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          if (j > lo && j - 1 >= half[w].lo && j - 1 < half[w].hi) {
-            ok = all(wait(&S.v_full[st ^ 1], (uint32_t)((n - 1) >> 1) & 1u, abort));
-#pragma unroll
-            for (int part = 0; part < 2 && ok; ++part) {
-              ok = all(wait(&S.p_full[w][part], (uint32_t)done[w] & 1u, abort));
-              if (!ok) break;
-              tc::tc_fence_after();
-              outputs(w, st ^ 1, done[w] == 0, part);
-            }
-            if (!ok) break;
-            if (++done[w] == half[w].hi - half[w].lo) commit(&S.o_full[w]);
-          }
-          if (j >= half[w].lo && j < half[w].hi) {
-            if (j == half[w].lo && !(ok = all(wait(&S.q_full[w], 0, abort)))) break;
-            tc::tc_fence_after();
-            scores(w, st);
-          }
-        }
-        if (!ok) break;
-        if (j < hi) commit(&S.k_empty[st]);
-        if (j > lo) commit(&S.v_empty[st ^ 1]);
+      // tiles that only the other half sees: passed on when they have come
+      auto skip = [&](int t) {
+        if (!full(S.k_full, t)) return false;
+        if (lane == 0) tc::mbar_arrive(&S.k_empty[t & 1]);
+        if (!full(S.v_full, t)) return false;
+        if (lane == 0) tc::mbar_arrive(&S.v_empty[t & 1]);
+        return true;
+      };
+      const int tiles = max(hi - lo, 0), seen = mine.hi - mine.lo, t0 = seen > 0 ? mine.lo - lo : tiles, t1 = t0 + seen;
+      bool ok = true;
+      for (int t = 0; t < t0 && ok; ++t) ok = skip(t);
+      if (ok && seen > 0 && (ok = all(wait(&S.q_full[w], 0, abort)) && full(S.k_full, t0))) {
+        tc::tc_fence_after();
+        scores(t0, 0);
+        scores(t0, 1);
+        commit(&S.k_empty[t0 & 1]);
       }
-      commit(&S.drained);
+      // The outputs of a step, then the scores of the step after next, into the place of the probabilities just used:
+      // while the tensor cores do that, the scores of the next step are ready for the softmax.
+      for (int t = t0; t < t1 && ok; ++t) {
+        const uint32_t ph = (uint32_t)(t - t0) & 1u;
+        const bool more = t + 1 < t1;
+        if (!(ok = full(S.v_full, t) && all(wait(&S.p_full[w][0], ph, abort)))) break;
+        tc::tc_fence_after();
+        outputs(t, 0, t == t0);
+        if (more) {
+          if (!(ok = full(S.k_full, t + 1))) break;
+          tc::tc_fence_after();
+          scores(t + 1, 0);
+        }
+        if (!(ok = all(wait(&S.p_full[w][1], ph, abort)))) break;
+        tc::tc_fence_after();
+        outputs(t, 1, false);
+        commit(&S.v_empty[t & 1]);
+        if (more) {
+          scores(t + 1, 1);
+          commit(&S.k_empty[(t + 1) & 1]);
+        }
+      }
+      for (int t = t1; t < tiles && ok; ++t) ok = skip(t);
+      commit(&S.drained[w]);
       // outstanding products read shared memory: wait (bounded) until they are done
-      const long long t0 = clock64();
-      while (!tc::mbar_try_wait(&S.drained, 0) && clock64() - t0 < tc::kSpinLimit) {
+      const long long c0 = clock64();
+      while (!tc::mbar_try_wait(&S.drained[w], 0) && clock64() - c0 < tc::kSpinLimit) {
       }
     } else if (warp == 13) {
       // ----- block scales -----
