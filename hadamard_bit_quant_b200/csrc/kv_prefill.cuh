@@ -72,9 +72,29 @@ HBL_DEVINL void commit(uint64_t* bar) {
       : "memory");
 }
 
-// tc::mbar_wait with the usual case, a phase that is over already, in front.
+// tc::mbar_wait, but the hardware holds the thread for up to a millisecond at a time: a warp that polls takes issue
+// slots from the softmax warps of its scheduler.
+HBL_DEVINL bool try_long(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(tc::su32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 HBL_DEVINL bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return tc::mbar_try_wait(bar, parity) || tc::mbar_wait(bar, parity, abort);
+  if (try_long(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!try_long(bar, parity)) {
+    if (*abort) return false;
+    if (clock64() - t0 > tc::kSpinLimit) {
+      *abort = 1;
+      set_device_error(HBL_ERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
 }
 
 // Instruction descriptor: D fp32, A and B fp16, M = 128, N = n; bit 16: B is MN-major.
@@ -109,6 +129,18 @@ HBL_DEVINL uint4 ldg_stream(const void* p) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
+}
+
+// As exp2_fast and pack_half, but kept in the order in which they are written.
+HBL_DEVINL float exp2_ordered(float x) {
+  float y;
+  asm volatile("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+HBL_DEVINL uint32_t pack_ordered(float lo, float hi) {
+  uint32_t r;
+  asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 HBL_DEVINL float max3(float a, float b, float c) {
@@ -349,26 +381,31 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         }
       }
       const float mu = m == -INFINITY ? 0.f : m;
+      // A pair's exponentials take the special function unit 16 cycles; the arithmetic of the pair kLag in front is issued
+      // in their shadow, in this order, and never waits for them.
+      constexpr int kPairs = kPreStep / 2, kLag = 4;
+      uint32_t p[16];
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t p[16];
-#pragma unroll
-        for (int g = 2 * c; g < 2 * c + 2; ++g) {
-          const float ag = add[g] - mu;
-          const float2 ff = make_float2(f[g], f[g]), aa = make_float2(ag, ag);
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[16 * g + 2 * i]),
-                                                    __uint_as_float(x[16 * g + 2 * i + 1])), ff, aa);
-            const float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
-            sum[i & 1] = __fadd2_rn(sum[i & 1], e);
-            p[8 * (g & 1) + i] = pack_half(e.x, e.y);
-          }
-          const float2 t = __fadd2_rn(sum[0], sum[1]);
-          l = __fmaf_rn(t.x + t.y, back[g], l);
+      for (int i = 0; i < kPairs + kLag; ++i) {
+        if (i < kPairs) {
+          const float ag = add[i >> 3] - mu;
+          const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
+                                      make_float2(f[i >> 3], f[i >> 3]), make_float2(ag, ag));
+          x[2 * i] = __float_as_uint(exp2_ordered(y.x));
+          x[2 * i + 1] = __float_as_uint(exp2_ordered(y.y));
         }
-        HBL_TMEM_ST16(src + 16u * c, p);
+        if (i >= kLag) {
+          const int q = i - kLag;
+          const float2 e = make_float2(__uint_as_float(x[2 * q]), __uint_as_float(x[2 * q + 1]));
+          p[q & 15] = pack_ordered(e.x, e.y);
+          sum[q & 1] = q & 6 ? __fadd2_rn(sum[q & 1], e) : e;
+          if ((q & 7) == 7) {
+            const float2 t = __fadd2_rn(sum[0], sum[1]);
+            l = __fmaf_rn(t.x + t.y, back[q >> 3], l);
+          }
+          if ((q & 15) == 15) HBL_TMEM_ST16(src + 16u * (q >> 4), p);
+        }
       }
       tc::tc_wait_st();
       tc::tc_fence_before();
@@ -518,31 +555,29 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       for (int t = 0; t < t0 && ok; ++t) ok = skip(t);
       if (ok && seen > 0 && (ok = all(wait(&S.q_full[w], 0, abort)) && full(S.k_full, t0))) {
         tc::tc_fence_after();
-        scores(t0, 0);
-        scores(t0, 1);
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) scores(t0, part);
         commit(&S.k_empty[t0 & 1]);
       }
       // The outputs of a step, then the scores of the step after next, into the place of the probabilities just used:
       // while the tensor cores do that, the scores of the next step are ready for the softmax.
-      for (int t = t0; t < t1 && ok; ++t) {
-        const uint32_t ph = (uint32_t)(t - t0) & 1u;
-        const bool more = t + 1 < t1;
-        if (!(ok = full(S.v_full, t) && all(wait(&S.p_full[w][0], ph, abort)))) break;
+      // One copy of the code for both steps of a tile: the warps of a block share the instruction caches.
+#pragma unroll 1
+      for (int n = 0; n < 2 * seen && ok; ++n) {
+        const int t = t0 + (n >> 1), part = n & 1;
+        if (part == 0) ok = full(S.v_full, t);
+        ok = ok && all(wait(&S.p_full[w][part], (uint32_t)(n >> 1) & 1u, abort));
+        if (!ok) break;
         tc::tc_fence_after();
-        outputs(t, 0, t == t0);
-        if (more) {
+        outputs(t, part, n == 0);
+        if (part) commit(&S.v_empty[t & 1]);
+        if (t + 1 == t1) continue;
+        if (part == 0) {
           if (!(ok = full(S.k_full, t + 1))) break;
           tc::tc_fence_after();
-          scores(t + 1, 0);
         }
-        if (!(ok = all(wait(&S.p_full[w][1], ph, abort)))) break;
-        tc::tc_fence_after();
-        outputs(t, 1, false);
-        commit(&S.v_empty[t & 1]);
-        if (more) {
-          scores(t + 1, 1);
-          commit(&S.k_empty[(t + 1) & 1]);
-        }
+        scores(t + 1, part);
+        if (part) commit(&S.k_empty[(t + 1) & 1]);
       }
       for (int t = t1; t < tiles && ok; ++t) ok = skip(t);
       commit(&S.drained[w]);
