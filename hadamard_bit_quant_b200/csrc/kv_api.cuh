@@ -58,10 +58,11 @@ int launch_kv_attention(const kv::AttnArgs& a, cudaStream_t s) {
       launch_pdl(kv::kv_prefill_kernel<D>, dim3((unsigned)(items * a.Hkv)), dim3(kv::kPreThreads), smem, s, a);
     }
   }
-  ensure_smem_attr(kv::kv_attn_kernel<D>, kv::AttnCfg<D>::kSmem);
   {
+    auto kernel = a.tile_rows == 8 ? kv::kv_attn_kernel<D, 1> : kv::kv_attn_kernel<D, 2>;
+    ensure_smem_attr(kernel, kv::AttnCfg<D>::kSmem);
     ProfScope ps("kv_attn", s);
-    launch_pdl(kv::kv_attn_kernel<D>, dim3(a.ctas), dim3(kv::kAttnWarps * 32), kv::AttnCfg<D>::kSmem, s, a);
+    launch_pdl(kernel, dim3(a.ctas), dim3(kv::kAttnWarps * 32), kv::AttnCfg<D>::kSmem, s, a);
   }
   {
     ProfScope ps("kv_combine", s);
@@ -179,12 +180,13 @@ int hbl_kv_attention(const hbl_bf16* Q, int T, int Hq, int Hkv, int D, long long
   DeviceState* d = nullptr;
   if ((st = ensure_device(&d))) return st;
   uint8_t* w = static_cast<uint8_t*>(ws);
-  const kv::AttnArgs a{Q, q_stride, cu_q, kv_lens, block_table, kcodes, vcodes, kscale, vscale, O, lse,
+  kv::AttnArgs a{Q, q_stride, cu_q, kv_lens, block_table, kcodes, vcodes, kscale, vscale, O, lse,
                        reinterpret_cast<long long*>(w + L.prefix), reinterpret_cast<float*>(w + L.ml),
                        reinterpret_cast<float*>(w + L.o), scale * kv::kLog2e, T, Hq, Hkv, Hq / Hkv, B, max_pages,
                        ilog2(page), num_pages, causal, window,
                        std::min(d->sm_count, kv::kMaxAttnCtas), std::max(kFewRows, Hq / Hkv),
-                       (int)std::min<long long>((long long)(max_q ? max_q : T) * (Hq / Hkv), 0x7fffffffll)};
+                       (int)std::min<long long>((long long)(max_q ? max_q : T) * (Hq / Hkv), 0x7fffffffll), 0};
+  a.tile_rows = std::min(a.most_rows, a.few_rows) <= 8 ? 8 : 16;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return D == 64 ? launch_kv_attention<64>(a, s) : launch_kv_attention<128>(a, s);
 }

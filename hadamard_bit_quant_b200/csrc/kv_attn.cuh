@@ -4,18 +4,21 @@
 // with k_j = (u_j - 128) * s of the key's block. Rows of one request that share a key/value head (its query
 // heads times its new tokens) are taken 16 at a time, so the cache is read once for all of them.
 //
-// The bound is the cache read: D bytes of keys and D of values for each token and head, with
-// 4 * 16 * D multiply-adds on them. The kernel is therefore a stream over tiles of 32 tokens:
+// The bound is the cache read: D bytes of keys and D of values for each token and head. The kernel is a stream over
+// tiles of 32 tokens:
 //   * one CTA per SM, each with an equal share of all tiles of all requests and heads (the long axis is
-//     split wherever the share ends), tiles dealt to 8 warps in turn;
-//   * each warp has a ring of its own in shared memory, filled with 16-byte cp.async, and its own running
-//     maximum, sum and output in registers: no barrier while it streams;
+//     split wherever the share ends), tiles dealt to 12 warps in turn;
+//   * each warp has a ring of its own in shared memory, filled with 16-byte cp.async, and its own reference
+//     maximum, sum and output in registers: no barrier while it streams. The next run's first tiles are fetched before
+//     the warps' results of this one are added up;
 //   * codes become fp16 exactly (0x6400 | u is 1024 + u; minus 1152), the query rows are scaled by a power of
 //     two into fp16's range (exact but for what lies 2^-25 below the row's largest value), and both products
-//     run on mma.m16n8k16 with fp32 sums. A 128-row tcgen05 tile would be at least 7/8 padding here;
-//   * a block's key scale multiplies the scores, its value scale the probabilities, relative to the largest
-//     value scale met so far, which keeps them inside fp16's range; they are rounded to fp16 (11 bits), finer than the
-//     bf16 output.
+//     run on mma.m16n8k16 with fp32 sums, the tokens (then the channels) as the 16 rows and the query rows as the 8
+//     columns: with 8 query rows nothing is padded, where a 128-row tcgen05 tile would be 15/16 padding;
+//   * a block's key scale multiplies the scores, its value scale the probabilities, relative to a reference value
+//     scale. Reference maximum and scale are raised only when a tile outgrows them by 2^8 and 16: then no
+//     lane has to ask the others for the tile's maximum. Probabilities stay below 2^12 and are rounded to fp16 (11
+//     bits), finer than the bf16 output.
 // At the end of a run the warps' results are added through shared memory. A run that is only a part of its
 // row's keys goes to the workspace, and kv_combine_kernel joins the parts.
 #pragma once
@@ -25,9 +28,11 @@
 namespace hbl {
 namespace kv {
 
-constexpr int kAttnWarps = 8;
+constexpr int kAttnWarps = 12;
 constexpr int kAttnTile = 32;         // tokens of a warp's tile
-constexpr int kAttnRows = 16;         // query rows of a tile
+constexpr int kAttnRows = 16;         // most query rows of a tile
+constexpr float kLag = 8.f;           // log2 of how far a tile may outgrow the reference maximum
+constexpr float kSlack = 16.f;        // and a value scale the reference scale
 constexpr int kMaxAttnCtas = 256;     // workspace is laid out for this many
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -51,6 +56,7 @@ struct AttnArgs {
   int T, Hq, Hkv, group, B, max_pages, page_log2, num_pages, causal, window, ctas;
   int few_rows;                       // requests with more rows per key/value head than this go to kv_prefill_kernel
   int most_rows;                      // and those with more than this break the caller's bound
+  int tile_rows;                      // query rows that kv_attn_kernel takes at a time: 8 or 16
 };
 
 // A request as the kernels see it: whatever the arrays hold, rows stay inside Q and keys inside the table.
@@ -66,7 +72,7 @@ HBL_DEVINL Request request_of(const AttnArgs& a, int b) {
   r.q = min(max(a.cu_q[b + 1], r.row0), a.T) - r.row0;
   r.kv = (int)min((long long)max(a.kv_lens[b], 0), (long long)a.max_pages << a.page_log2);
   r.few = (long long)r.q * a.group <= a.few_rows;
-  r.rt = (int)(((long long)r.q * a.group + kAttnRows - 1) / kAttnRows);
+  r.rt = (int)(((long long)r.q * a.group + a.tile_rows - 1) / a.tile_rows);
   // tiles from the first key that any of its rows sees to the last
   r.lo = a.window > 0 ? max(r.kv - r.q + 1 - a.window, 0) / kAttnTile : 0;
   r.tiles = r.q > 0 && r.few ? (r.kv + kAttnTile - 1) / kAttnTile - r.lo : 0;
@@ -94,6 +100,11 @@ HBL_DEVINL uint4 lds128(uint32_t a) {
 HBL_DEVINL uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+HBL_DEVINL float2 lds64f(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];\n" : "=f"(v.x), "=f"(v.y) : "r"(a));
   return v;
 }
 HBL_DEVINL float lds32f(uint32_t a) {
@@ -137,36 +148,47 @@ HBL_DEVINL void row_power(float amax, float* up, float* down) {
 }
 
 // Shared memory of a CTA: each warp's ring of stages (32 tokens of keys, then of values, and 4 scales),
-// then the buffer through which the warps' outputs are added.
+// then the buffer through which the warps' outputs are added, four rows at a time.
 template <int D> struct AttnCfg {
   static constexpr int kKBytes = kAttnTile * D;
   static constexpr int kStageBytes = 2 * kKBytes + 16;
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kRing = kAttnWarps * kStages * kStageBytes;
-  static constexpr int kMerge = kAttnWarps * 8 * D * 4;
+  static constexpr int kMerge = kAttnWarps * 4 * D * 4;
   static constexpr int kSmem = kRing + kMerge + kAttnWarps * kAttnRows * 8;
 };
 
-// 16-byte chunk c of token row r of a tile lies at chunk c ^ swz(r): the key reads (rows 4g + i, chunks t)
-// and the value reads (rows 8t + e, chunk g) of a quarter-warp then fall on different banks.
-template <int D> HBL_DEVINL uint32_t tile_at(int r, int c) {
-  if constexpr (D == 128) return (uint32_t)(r * 128 + ((c ^ (r & 7) ^ ((r >> 3) << 1)) & 7) * 16);
-  else return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3) ^ (r >> 3)) & 3) * 16);
+// 16-byte chunk c of token row r of a tile lies at chunk c ^ swz(r), chosen for the reads of a quarter-warp (two
+// neighbouring g, four t): keys are read as rows g, chunks t, values as rows 2t + e, chunks g. With 8 chunks to a row
+// both then touch every bank once; with 4 chunks the keys do, the values twice.
+template <int D> HBL_DEVINL constexpr uint32_t swz(int r) {
+  return D == 128 ? (uint32_t)((((r ^ (r >> 2)) & 1) << 2) | (r & 2)) : (uint32_t)((r >> 1) & 3);
+}
+template <int D> HBL_DEVINL uint32_t tile_at(int r, int c) { return (uint32_t)(r * D) + (((uint32_t)c ^ swz<D>(r)) << 4); }
+
+HBL_DEVINL uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
 }
 
-template <int D>
+// Consecutive tiles [lo, hi) of one request, head and row tile, taken by one CTA.
+struct Run {
+  Request rq;
+  int b, h, rt, lo, hi;
+};
+
+template <int D, int NT>   // NT: column tiles of 8 query rows
 __global__ void __launch_bounds__(kAttnWarps * 32, 1) kv_attn_kernel(const AttnArgs a) {
   using C = AttnCfg<D>;
   constexpr int NK = D / 16;          // k-steps of the score product
-  constexpr int NJ = D / 8;           // column tiles of the output
-  constexpr int CPR = D / 16;         // 16-byte chunks of a token row
+  constexpr int NJ = D / 16;          // row tiles of the output product
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long sh[9];
+  __shared__ long long sh[kAttnWarps];
   __shared__ int s_b;
   __shared__ long long s_off;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t4 = lane & 3;
-  const int P = 1 << a.page_log2;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
 
   // this CTA's share [w0, w1) of all tiles, and the request in which it begins
@@ -212,47 +234,103 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) kv_attn_kernel(const AttnA
 
   uint8_t* ring = smem + warp * (C::kStages * C::kStageBytes);
   const uint32_t ring_u = (uint32_t)__cvta_generic_to_shared(ring);
-  float* merge = reinterpret_cast<float*>(smem + C::kRing);                        // [warp][8][D], chunks permuted
-  float2* merge_ml = reinterpret_cast<float2*>(smem + C::kRing + C::kMerge);       // [warp][16]
+  float* merge = reinterpret_cast<float*>(smem + C::kRing);                        // [warp][4][D], chunks permuted
+  float2* merge_ml = reinterpret_cast<float2*>(smem + C::kRing + C::kMerge);       // [warp][8 NT]
 
-  int b = s_b;
-  Request rq = request_of(a, b);
-  long long at = s_off;               // tile within the request, over (head, row tile, tile)
-  bool first_item = true;
-  for (long long w = w0; w < w1;) {
-    while (at >= tiles_of(a, rq)) {   // the next request with any tiles
+  // The run at tile `at` of request r.b, with `left` tiles of the CTA's share to go.
+  Run run;
+  run.b = s_b;
+  run.rq = request_of(a, run.b);
+  long long at = s_off, left = w1 - w0;
+  auto open = [&](Run& r) {
+    while (at >= tiles_of(a, r.rq)) {   // the next request with any tiles
       at = 0;
-      rq = request_of(a, ++b);
+      r.rq = request_of(a, ++r.b);
     }
-    const int item = (int)(at / rq.tiles), lo = (int)(at % rq.tiles);
-    const int h = item / rq.rt, rt = item % rq.rt;
-    const int hi = (int)min((long long)rq.tiles, lo + (w1 - w));
-    // tiles [lo, hi) of this item; token tile j starts at key (rq.lo + j) * 32
-    const int row_lo = rt * kAttnRows, rows = min(kAttnRows, rq.q * a.group - row_lo);
-    // keys that row r of the tile sees: [first, last)
-    int first[2], last[2], tok[2], head[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = min(row_lo + g + 8 * i, rq.q * a.group - 1);
-      tok[i] = r / a.group;
-      head[i] = h * a.group + r % a.group;
-      const int pos = rq.kv - rq.q + tok[i];
-      last[i] = a.causal ? max(min(rq.kv, pos + 1), 0) : rq.kv;
-      first[i] = a.window > 0 ? max(pos + 1 - a.window, 0) : 0;
-    }
-    // keys that every row of the tile sees
-    const int tok_a = row_lo / a.group, tok_b = (row_lo + rows - 1) / a.group;
-    const int all_last = a.causal ? min(rq.kv, rq.kv - rq.q + tok_a + 1) : rq.kv;
-    const int any_last = a.causal ? min(rq.kv, rq.kv - rq.q + tok_b + 1) : rq.kv;
-    const int all_first = a.window > 0 ? max(rq.kv - rq.q + tok_b + 1 - a.window, 0) : 0;
-    const int any_first = a.window > 0 ? max(rq.kv - rq.q + tok_a + 1 - a.window, 0) : 0;
+    const int item = (int)(at / r.rq.tiles);
+    r.lo = (int)(at % r.rq.tiles);
+    r.h = item / r.rq.rt;
+    r.rt = item % r.rq.rt;
+    r.hi = (int)min((long long)r.rq.tiles, r.lo + left);
+    at += r.hi - r.lo;
+    left -= r.hi - r.lo;
+  };
 
-    // query fragments, scaled by a power of two into fp16
-    uint32_t qf[NK][4];
-    float qs[2];
+  // Copies of one tile: 32 token rows of keys and of values, and the scales of its (at most two) pages. Rows behind
+  // the last key are not fetched; a page outside the cache is recorded, its scales marked -1, which masks its keys. A
+  // tile's half lies within one page, so its chunks are consecutive in memory and the offsets below constants.
+  const uint32_t dst0 = tile_at<D>(lane / (D / 16), lane % (D / 16));                       // of even copies
+  const uint32_t dst1 = tile_at<D>(lane / (D / 16) + 512 / D, lane % (D / 16)) - 512u;      // of odd ones
+  const uint32_t block = (uint32_t)D << a.page_log2, step = block * (uint32_t)a.Hkv;        // bytes of a page's head, of a page
+  const uint32_t pmask = (1u << a.page_log2) - 1u;
+  auto issue = [&](const Run& r, int j, int stage) {
+    const uint32_t s0 = ring_u + stage * C::kStageBytes;
+    const int key0 = (r.rq.lo + j) * kAttnTile;
+    const int32_t* table = a.table + (size_t)r.b * a.max_pages;
+    int id[2];
+    id[0] = __ldg(table + (key0 >> a.page_log2));
+    id[1] = key0 + 16 < r.rq.kv ? __ldg(table + ((key0 + 16) >> a.page_log2)) : 0;
+    bool ok[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint16_t* q = a.Q + (size_t)(rq.row0 + tok[i]) * (size_t)a.q_stride + (size_t)head[i] * D;
+    for (int e = 0; e < 2; ++e) {
+      ok[e] = id[e] >= 0 && id[e] < a.num_pages;
+      if (!ok[e]) set_device_error(HBL_ERR_INVALID_ARG);
+    }
+    if (lane < 4) {
+      const int e = lane & 1;
+      const uint32_t dst = s0 + 2 * C::kKBytes + 4 * lane;
+      if (e ? ok[1] : ok[0])
+        cp_async4(dst, (lane < 2 ? a.kscale : a.vscale) + (size_t)(e ? id[1] : id[0]) * a.Hkv + r.h);
+      else
+        asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(dst), "f"(-1.f) : "memory");
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (!ok[e]) continue;
+      const int key = key0 + 16 * e;
+      const uint64_t src = (uint64_t)(uint32_t)id[e] * step + (uint64_t)r.h * block + ((uint32_t)key & pmask) * D + 16 * lane;
+      const uint8_t *ks = a.kcodes + src, *vs = a.vcodes + src;
+      const int rows = r.rq.kv - key;                       // keys of this half and behind it
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        const uint32_t dst = s0 + 16 * e * D + 512 * k + ((k & 1) ? dst1 : dst0);
+        if (512 * k / D + lane / (D / 16) < rows) {
+          cp_async16(dst, ks + 512 * k);
+          cp_async16(dst + C::kKBytes, vs + 512 * k);
+        }
+      }
+    }
+  };
+  auto fill = [&](const Run& r) {
+#pragma unroll
+    for (int s = 0; s < C::kStages - 1; ++s) {
+      const int j = r.lo + warp + s * kAttnWarps;
+      if (j < r.hi) issue(r, j, s);
+      cp_commit();
+    }
+  };
+
+  open(run);
+  fill(run);
+  bool first_item = true;
+  while (true) {
+    const Request& rq = run.rq;
+    const int row_lo = run.rt * 8 * NT, rows = min(8 * NT, rq.q * a.group - row_lo);
+    // keys that every row, and that any row, of the tile sees
+    const int tok_a = row_lo / a.group, tok_b = (row_lo + rows - 1) / a.group, pos0 = rq.kv - rq.q;
+    const int all_last = a.causal ? min(rq.kv, pos0 + tok_a + 1) : rq.kv;
+    const int any_last = a.causal ? min(rq.kv, pos0 + tok_b + 1) : rq.kv;
+    const int all_first = a.window > 0 ? max(pos0 + tok_b + 1 - a.window, 0) : 0;
+    const int any_first = a.window > 0 ? max(pos0 + tok_a + 1 - a.window, 0) : 0;
+
+    // query fragments: row g of each column tile, scaled by a power of two into fp16
+    uint32_t qf[NT][NK][2];
+    float qs[NT][2];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int r = min(row_lo + 8 * i + g, rq.q * a.group - 1);
+      const uint16_t* q = a.Q + (size_t)(rq.row0 + r / a.group) * (size_t)a.q_stride +
+                          (size_t)(run.h * a.group + r % a.group) * D;
       uint32_t raw[NK][2];
       float amax = 0.f;
 #pragma unroll
@@ -274,156 +352,149 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) kv_attn_kernel(const AttnA
                                    fabsf(__uint_as_float(raw[k][e] & 0xffff0000u))));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      float up;
-      row_power(amax, &up, &qs[i]);
-      qs[i] *= a.scale_log2;
+      float up, down;
+      row_power(amax, &up, &down);
+      down *= a.scale_log2;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) qs[i][e] = __shfl_sync(0xffffffffu, down, 8 * t4 + 4 * e);   // of rows 2 t4 + e
 #pragma unroll
       for (int k = 0; k < NK; ++k)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          qf[k][2 * e + i] = pack_half(__uint_as_float(raw[k][e] << 16) * up,
-                                       __uint_as_float(raw[k][e] & 0xffff0000u) * up);
+          qf[i][k][e] = pack_half(__uint_as_float(raw[k][e] << 16) * up, __uint_as_float(raw[k][e] & 0xffff0000u) * up);
     }
 
-    float o[NJ][4];
+    // this thread's rows are 8 i + 2 t4 + e; output tile jj holds the channels 2 NJ g + 2 jj and the next one
+    float o[NT][NJ][4], m[NT][2], l[NT][2], vref = 0.f;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
+    for (int i = 0; i < NT; ++i) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, vref = 0.f;
-
-    // Copies of one tile: 32 token rows of keys and of values, and the scales of its (at most two) pages.
-    // A page outside the cache is recorded and its scales marked -1, which masks its keys.
-    const int32_t* table = a.table + (size_t)b * a.max_pages;
-    auto issue = [&](int j, int stage) {
-      const uint32_t s0 = ring_u + stage * C::kStageBytes;
-      const int key0 = (rq.lo + j) * kAttnTile;
-      int id[2];
+      for (int jj = 0; jj < NJ; ++jj)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int key = key0 + 16 * e;
-        id[e] = key < rq.kv ? __ldg(table + (key >> a.page_log2)) : 0;
-        if (id[e] < 0 || id[e] >= a.num_pages) {
-          set_device_error(HBL_ERR_INVALID_ARG);
-          id[e] = -1;
-        }
-      }
-      if (lane < 4) {
-        const int p = id[lane & 1];
-        const uint32_t dst = s0 + 2 * C::kKBytes + 4 * lane;
-        if (p >= 0) cp_async4(dst, (lane < 2 ? a.kscale : a.vscale) + (size_t)p * a.Hkv + h);
-        else asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(dst), "f"(-1.f) : "memory");
-      }
-#pragma unroll
-      for (int k = 0; k < CPR; ++k) {
-        const int i = lane + 32 * k, r = i / CPR, c = i % CPR, key = key0 + r;
-        const int p = id[r >> 4];
-        if (key < rq.kv && p >= 0) {
-          const size_t src = ((((size_t)p * a.Hkv + h) << a.page_log2) + (size_t)(key & (P - 1))) * D + 16 * c;
-          cp_async16(s0 + tile_at<D>(r, c), a.kcodes + src);
-          cp_async16(s0 + C::kKBytes + tile_at<D>(r, c), a.vcodes + src);
-        }
-      }
-    };
-
-    const int j0 = lo + warp;
-#pragma unroll
-    for (int s = 0; s < C::kStages - 1; ++s) {
-      if (j0 + s * kAttnWarps < hi) issue(j0 + s * kAttnWarps, s);
-      cp_commit();
+        for (int e = 0; e < 4; ++e) o[i][jj][e] = 0.f;
+      m[i][0] = m[i][1] = -INFINITY;
+      l[i][0] = l[i][1] = 0.f;
     }
+
     int stage = 0;
-    for (int j = j0; j < hi; j += kAttnWarps) {
+    for (int j = run.lo + warp; j < run.hi; j += kAttnWarps) {
       const int ahead = j + (C::kStages - 1) * kAttnWarps;
-      if (ahead < hi) issue(ahead, stage == 0 ? C::kStages - 1 : stage - 1);
+      if (ahead < run.hi) issue(run, ahead, stage == 0 ? C::kStages - 1 : stage - 1);
       cp_commit();
       cp_wait<C::kStages - 1>();
       __syncwarp();
       const uint32_t s0 = ring_u + stage * C::kStageBytes;
       const int key0 = (rq.lo + j) * kAttnTile;
       if (key0 < any_last && key0 + kAttnTile > any_first) {
-        // scores: tile i holds the keys 4c + i of its columns c
-        float s[4][4];
+        // scores: token tile h holds the keys key0 + 16 h + g and 8 more of its rows, and lies within a page
+        float s[NT][2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int c = 0; c < NK / 4; ++c) {
-            const uint4 w = lds128(s0 + tile_at<D>(4 * g + i, t4 + 4 * c));
-            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+          for (int hh = 0; hh < 2; ++hh) s[i][hh][0] = s[i][hh][1] = s[i][hh][2] = s[i][hh][3] = 0.f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f16(s[i], qf[4 * c + k], codes_lo(ws[k]), codes_hi(ws[k]));
+        for (int c = 0; c < NK / 4; ++c)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const uint4 x = lds128(s0 + tile_at<D>(16 * hh + g, t4 + 4 * c)), y = lds128(s0 + tile_at<D>(16 * hh + g + 8, t4 + 4 * c));
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t kf[4] = {codes_lo(xs[k]), codes_lo(ys[k]), codes_hi(xs[k]), codes_hi(ys[k])};
+#pragma unroll
+              for (int i = 0; i < NT; ++i) mma_f16(s[i][hh], kf, qf[i][4 * c + k][0], qf[i][4 * c + k][1]);
+            }
           }
-        }
-        // this thread's keys are 8 t4 .. 8 t4 + 7, all of one page
-        const float ks = lds32f(s0 + 2 * C::kKBytes + 4 * (t4 >> 1));
-        float vs = lds32f(s0 + 2 * C::kKBytes + 8 + 4 * (t4 >> 1));
-        const int key = key0 + 8 * t4;
-        const bool whole = key0 >= all_first && key0 + kAttnTile <= all_last && !__any_sync(0xffffffffu, ks < 0.f);
-        const float f[2] = {qs[0] * ks, qs[1] * ks};
+        const float2 ks = lds64f(s0 + 2 * C::kKBytes);
+        float2 vs = lds64f(s0 + 2 * C::kKBytes + 8);
+        const bool whole = key0 >= all_first && key0 + kAttnTile <= all_last && ks.x >= 0.f && ks.y >= 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[i][e] *= f[e >> 1];
+          for (int e = 0; e < 4; ++e) {
+            s[i][0][e] *= ks.x * qs[i][e & 1];
+            s[i][1][e] *= ks.y * qs[i][e & 1];
+          }
         if (!whole) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int k = key + i + 4 * (e & 1);
-              if (k < first[e >> 1] || k >= last[e >> 1] || ks < 0.f) s[i][e] = -INFINITY;
+            for (int e = 0; e < 2; ++e) {
+              const int pos = pos0 + min(row_lo + 8 * i + 2 * t4 + e, rq.q * a.group - 1) / a.group;
+              const int last = a.causal ? min(rq.kv, pos + 1) : rq.kv;
+              const int first = a.window > 0 ? pos + 1 - a.window : 0;
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                  const int key = key0 + 16 * hh + 8 * f + g;
+                  if (key < first || key >= last || (hh ? ks.y : ks.x) < 0.f) s[i][hh][2 * f + e] = -INFINITY;
+                }
+            }
+          // a half of which no row sees anything: its page's scale says nothing
+          if (key0 >= any_last || key0 + 16 <= any_first || ks.x < 0.f) vs.x = 0.f;
+          if (key0 + 16 >= any_last || key0 + 32 <= any_first || ks.y < 0.f) vs.y = 0.f;
+        }
+        // references: raised when any lane's scores, or a value scale, have outgrown them
+        const float vmax = fmaxf(vs.x, vs.y);
+        bool grown = vmax > kSlack * vref;
+        float x[NT][2];
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            x[i][e] = fmaxf(fmaxf(s[i][0][e], s[i][0][e + 2]), fmaxf(s[i][1][e], s[i][1][e + 2]));
+            grown |= x[i][e] > m[i][e] + kLag;
+          }
+        if (__any_sync(0xffffffffu, grown)) {
+          const float vnew = vmax > kSlack * vref ? vmax : vref;
+          const float shrink = vnew == vref ? 1.f : __fdividef(vref, vnew);
+          vref = vnew;
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float y = x[i][e];
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+              const float mn = fmaxf(m[i][e], y);
+              const float alpha = mn == m[i][e] ? 1.f : exp2_fast(m[i][e] - mn);
+              m[i][e] = mn;
+              l[i][e] *= alpha;
+#pragma unroll
+              for (int jj = 0; jj < NJ; ++jj) {
+                o[i][jj][e] *= alpha * shrink;
+                o[i][jj][e + 2] *= alpha * shrink;
+              }
             }
         }
-        // a half tile of which no row sees anything: its page's scale says nothing
-        const int half0 = key0 + 16 * (t4 >> 1);
-        if (half0 >= any_last || half0 + 16 <= any_first || ks < 0.f) vs = 0.f;
-        float vmax = fmaxf(vs, __shfl_xor_sync(0xffffffffu, vs, 2));
-        const float vnew = fmaxf(vref, vmax);
-        const float vr = vnew > 0.f ? __fdividef(vs, vnew) : 0.f;
-        const float shrink = vref == vnew ? 1.f : __fdividef(vref, vnew);
-        vref = vnew;
-        float alpha[2], mu[2];
+        const float inv = vref > 0.f ? __fdividef(1.f, vref) : 0.f;
+        const float vr[2] = {vs.x * inv, vs.y * inv};
+        uint32_t pf[NT][2][2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = fmaxf(fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1])),
-                          fmaxf(fmaxf(s[2][2 * e], s[2][2 * e + 1]), fmaxf(s[3][2 * e], s[3][2 * e + 1])));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          const float mn = fmaxf(m[e], x);
-          mu[e] = mn == -INFINITY ? 0.f : mn;
-          alpha[e] = exp2_fast(m[e] - mu[e]);
-          m[e] = mn;
-        }
-        uint32_t pf[2][4];
-        float ls[2] = {0.f, 0.f};
+        for (int i = 0; i < NT; ++i) {
+          const float mu[2] = {m[i][0] == -INFINITY ? 0.f : m[i][0], m[i][1] == -INFINITY ? 0.f : m[i][1]};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float p[4];
+          for (int hh = 0; hh < 2; ++hh) {
+            float p[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            p[e] = exp2_fast(s[i][e] - mu[e >> 1]);
-            ls[e >> 1] += p[e];
-            p[e] *= vr;
+            for (int e = 0; e < 4; ++e) {
+              p[e] = exp2_fast(s[i][hh][e] - mu[e & 1]);
+              l[i][e & 1] += p[e];
+              p[e] *= vr[hh];
+            }
+            // a token's two rows side by side; transposed, a row's two tokens
+            pf[i][hh][0] = transpose8(pack_half(p[0], p[1]));
+            pf[i][hh][1] = transpose8(pack_half(p[2], p[3]));
           }
-          pf[i >> 1][2 * (i & 1)] = pack_half(p[0], p[1]);
-          pf[i >> 1][2 * (i & 1) + 1] = pack_half(p[2], p[3]);
         }
-        l[0] = l[0] * alpha[0] + ls[0];
-        l[1] = l[1] * alpha[1] + ls[1];
-        const float ao[2] = {alpha[0] * shrink, alpha[1] * shrink};
-        if (__any_sync(0xffffffffu, ao[0] != 1.f || ao[1] != 1.f)) {
+        // outputs, 16 tokens at a time: this thread reads the tokens 2 t4 + {0, 1, 8, 9}, channels 2 NJ g and on
 #pragma unroll
-          for (int jj = 0; jj < NJ; ++jj)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[jj][e] *= ao[e >> 1];
-        }
-        // output: column tile jj holds the channels NJ * c + jj of its columns c
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {            // keys 8 t4 + {0, 4, 1, 5}, then {2, 6, 3, 7}
-          uint32_t v[4][NJ / 4];
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t v[4][NJ / 2];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int r = 8 * t4 + 2 * half + (e >> 1) + 4 * (e & 1);
+            const int r = 16 * hh + 2 * t4 + (e & 1) + 8 * (e >> 1);
             if constexpr (D == 128) {
               const uint4 w = lds128(s0 + C::kKBytes + tile_at<D>(r, g));
               v[e][0] = w.x; v[e][1] = w.y; v[e][2] = w.z; v[e][3] = w.w;
@@ -433,80 +504,90 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) kv_attn_kernel(const AttnA
             }
           }
 #pragma unroll
-          for (int k = 0; k < NJ / 4; ++k) {
-            const uint32_t a0 = __byte_perm(v[0][k], v[1][k], 0x5140), a1 = __byte_perm(v[0][k], v[1][k], 0x7362);
-            const uint32_t b0 = __byte_perm(v[2][k], v[3][k], 0x5140), b1 = __byte_perm(v[2][k], v[3][k], 0x7362);
-            mma_f16(o[4 * k + 0], pf[half], codes_lo(a0), codes_lo(b0));
-            mma_f16(o[4 * k + 1], pf[half], codes_hi(a0), codes_hi(b0));
-            mma_f16(o[4 * k + 2], pf[half], codes_lo(a1), codes_lo(b1));
-            mma_f16(o[4 * k + 3], pf[half], codes_hi(a1), codes_hi(b1));
-          }
+          for (int k = 0; k < NJ / 2; ++k)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {                   // channels 4 k + 2 f and the next
+              const uint32_t sel = f ? 0x7362 : 0x5140;
+              const uint32_t c0 = __byte_perm(v[0][k], v[1][k], sel), c8 = __byte_perm(v[2][k], v[3][k], sel);
+              const uint32_t vf[4] = {codes_lo(c0), codes_hi(c0), codes_lo(c8), codes_hi(c8)};
+#pragma unroll
+              for (int i = 0; i < NT; ++i) mma_f16(o[i][2 * k + f], vf, pf[i][hh][0], pf[i][hh][1]);
+            }
         }
       }
       __syncwarp();
       stage = stage + 1 == C::kStages ? 0 : stage + 1;
     }
+    // the ring is this run's no longer
+    const bool more = left > 0;
+    Run next = run;
     cp_wait<0>();
     __syncwarp();
+    if (more) {
+      open(next);
+      fill(next);
+    }
 
     // add the warps' results
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-      if (t4 == 0) merge_ml[warp * kAttnRows + g + 8 * e] = make_float2(m[e], l[e]);
-    }
-    const bool final_ = lo == 0 && hi == rq.tiles;
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], d);
+        if (g == 0) merge_ml[warp * 8 * NT + 8 * i + 2 * t4 + e] = make_float2(m[i][e], l[i][e]);
+      }
+    const bool final_ = run.lo == 0 && run.hi == rq.tiles;
     const size_t slot = ((size_t)blockIdx.x * 2 + (first_item ? 0 : 1)) * kAttnRows;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      // rows 8e .. 8e + 7: this thread's channels are 2 NJ t4 + jj (columns 2 t4) and NJ more; 16-byte chunk c
-      // of that run of 2 NJ lies at c ^ (4 (g & 1) + t4)
-      if (8 * e < rows) {
+    for (int pass = 0; pass < 2 * NT; ++pass) {             // rows 4 pass .. 4 pass + 3
+      if (4 * pass >= rows) break;
+      if ((t4 >> 1) == (pass & 1)) {
 #pragma unroll
-        for (int c = 0; c < NJ / 2; ++c) {
-          const int jj = 4 * (c % (NJ / 4)), col = c / (NJ / 4);
-          const float4 v = make_float4(o[jj][2 * e + col] * vref, o[jj + 1][2 * e + col] * vref,
-                                       o[jj + 2][2 * e + col] * vref, o[jj + 3][2 * e + col] * vref);
-          const int pc = c ^ ((4 * (g & 1) + t4) & (NJ / 2 - 1));
-          *reinterpret_cast<float4*>(merge + (warp * 8 + g) * D + 2 * NJ * t4 + 4 * pc) = v;
+        for (int e = 0; e < 2; ++e) {
+          float* dst = merge + (warp * 4 + 2 * (t4 & 1) + e) * D;
+#pragma unroll
+          for (int c = 0; c < NJ / 2; ++c) {
+            const auto& u = o[pass >> 1][2 * c];
+            const auto& w = o[pass >> 1][2 * c + 1];
+            const int ch = (NJ / 2) * g + c;                // chunk of four channels, moved by the row pair
+            *reinterpret_cast<float4*>(dst + 4 * (ch ^ (t4 & 1))) =
+                make_float4(u[e] * vref, u[e + 2] * vref, w[e] * vref, w[e + 2] * vref);
+          }
         }
       }
       __syncthreads();
-      if (8 * e < rows) {
-        for (int i = threadIdx.x; i < 8 * (D / 4); i += blockDim.x) {
-          const int gr = i / (D / 4), ch = i % (D / 4), r = 8 * e + gr;
-          if (r < rows) {
-            const int tt = ch / (NJ / 2), pc = (ch % (NJ / 2)) ^ ((4 * (gr & 1) + tt) & (NJ / 2 - 1));
-            float M = -INFINITY, L = 0.f;
+      for (int i = threadIdx.x; i < D; i += blockDim.x) {   // 4 rows x D / 4 chunks
+        const int rr = i / (D / 4), ch = i % (D / 4), r = 4 * pass + rr;
+        if (r < rows) {
+          float M = -INFINITY, L = 0.f;
 #pragma unroll
-            for (int k = 0; k < kAttnWarps; ++k) M = fmaxf(M, merge_ml[k * kAttnRows + r].x);
-            const float mu = M == -INFINITY ? 0.f : M;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int k = 0; k < kAttnWarps; ++k) M = fmaxf(M, merge_ml[k * 8 * NT + r].x);
+          const float mu = M == -INFINITY ? 0.f : M;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < kAttnWarps; ++k) {
-              const float2 ml = merge_ml[k * kAttnRows + r];
-              const float f = exp2_fast(ml.x - mu);
-              const float4 v = *reinterpret_cast<const float4*>(merge + (k * 8 + gr) * D + 2 * NJ * tt + 4 * pc);
-              L += ml.y * f;
-              acc.x += v.x * f; acc.y += v.y * f; acc.z += v.z * f; acc.w += v.w * f;
-            }
-            const int d = 4 * ch;
-            if (final_) {
-              const int rr = row_lo + r;
-              const size_t out = (size_t)(rq.row0 + rr / a.group) * a.Hq + (size_t)(h * a.group + rr % a.group);
-              const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-              uint2 y;
-              y.x = (uint32_t)float_to_bf16_bits(acc.x * inv) | ((uint32_t)float_to_bf16_bits(acc.y * inv) << 16);
-              y.y = (uint32_t)float_to_bf16_bits(acc.z * inv) | ((uint32_t)float_to_bf16_bits(acc.w * inv) << 16);
-              *reinterpret_cast<uint2*>(a.O + out * D + d) = y;
-              if (a.lse && ch == 0) a.lse[out] = L > 0.f || L != L ? M * kLn2 + logf(L) : -INFINITY;
-            } else {
-              *reinterpret_cast<float4*>(a.part_o + (slot + r) * D + d) = acc;
-              if (ch == 0) {
-                a.part_ml[2 * (slot + r)] = M;
-                a.part_ml[2 * (slot + r) + 1] = L;
-              }
+          for (int k = 0; k < kAttnWarps; ++k) {
+            const float2 ml = merge_ml[k * 8 * NT + r];
+            const float f = exp2_fast(ml.x - mu);
+            const float4 v = *reinterpret_cast<const float4*>(merge + (k * 4 + rr) * D + 4 * (ch ^ (rr >> 1)));
+            L += ml.y * f;
+            acc.x += v.x * f; acc.y += v.y * f; acc.z += v.z * f; acc.w += v.w * f;
+          }
+          const int d = 4 * ch;
+          if (final_) {
+            const int row = row_lo + r;
+            const size_t out = (size_t)(rq.row0 + row / a.group) * a.Hq + (size_t)(run.h * a.group + row % a.group);
+            const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+            uint2 y;
+            y.x = (uint32_t)float_to_bf16_bits(acc.x * inv) | ((uint32_t)float_to_bf16_bits(acc.y * inv) << 16);
+            y.y = (uint32_t)float_to_bf16_bits(acc.z * inv) | ((uint32_t)float_to_bf16_bits(acc.w * inv) << 16);
+            *reinterpret_cast<uint2*>(a.O + out * D + d) = y;
+            if (a.lse && ch == 0) a.lse[out] = L > 0.f || L != L ? M * kLn2 + logf(L) : -INFINITY;
+          } else {
+            *reinterpret_cast<float4*>(a.part_o + (slot + r) * D + d) = acc;
+            if (ch == 0) {
+              a.part_ml[2 * (slot + r)] = M;
+              a.part_ml[2 * (slot + r) + 1] = L;
             }
           }
         }
@@ -514,8 +595,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) kv_attn_kernel(const AttnA
       __syncthreads();
     }
     first_item = false;
-    w += hi - lo;
-    at += hi - lo;
+    if (!more) break;
+    run = next;
   }
 }
 
@@ -531,7 +612,7 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const AttnArgs a, const
   const Request rq = request_of(a, lo);
   if (r == 0 && h == 0 && lane == 0 && (long long)rq.q * a.group > a.most_rows) set_device_error(HBL_ERR_INVALID_ARG);
   if (!rq.few || r >= rq.q * a.group) return;
-  const int rt = r / kAttnRows;
+  const int rt = r / a.tile_rows;
   const size_t row = (size_t)(rq.row0 + r / a.group) * a.Hq + (size_t)(h * a.group + r % a.group);
   float M = -INFINITY, L = 0.f;
   constexpr int V = D / 32;                                 // channels of a lane
@@ -546,7 +627,7 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const AttnArgs a, const
     if (c0 == c1) return;                                   // written by that CTA
     for (int c = c0; c <= c1; ++c) {
       const bool begins = c > c0 || total * c / n == x0;   // the CTA's first item, or its last
-      const size_t slot = ((size_t)c * 2 + (begins ? 0 : 1)) * kAttnRows + r % kAttnRows;
+      const size_t slot = ((size_t)c * 2 + (begins ? 0 : 1)) * kAttnRows + r % a.tile_rows;
       const float m = a.part_ml[2 * slot], l = a.part_ml[2 * slot + 1];
       const float mn = fmaxf(M, m), mu = mn == -INFINITY ? 0.f : mn;
       const float f0 = exp2_fast(M - mu), f1 = exp2_fast(m - mu);
