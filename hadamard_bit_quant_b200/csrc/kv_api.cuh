@@ -43,6 +43,9 @@ KvWs kv_ws_layout(int B, int D) {
 // Rows per key/value head up to which a request is streamed by kv_attn_kernel; more go to the tensor-core kernel.
 constexpr int kFewRows = 32;
 
+// Most cached tokens of a request, and most CTAs, for which kv_attn_kernel leaves each item to one CTA.
+constexpr int kWholeKeys = 512, kWholeCtas = 4096;
+
 // Three kernels, each of which takes the requests that are its own: which those are is known on the GPU only.
 // The host leaves out what its bound on the rows rules out.
 template <int D>
@@ -64,10 +67,11 @@ int launch_kv_attention(const kv::AttnArgs& a, cudaStream_t s) {
     ProfScope ps("kv_attn", s);
     launch_pdl(kernel, dim3(a.ctas), dim3(kv::kAttnWarps * 32), kv::AttnCfg<D>::kSmem, s, a);
   }
-  {
+  if (a.row_tiles == 0) {
     ProfScope ps("kv_combine", s);
     const int rows = std::min(a.few_rows, a.most_rows);
-    launch_pdl(kv::kv_combine_kernel<D>, dim3((unsigned)(((long long)a.B * a.Hkv * rows + 7) / 8)), dim3(256), 0, s, a,
+    launch_pdl(kv::kv_combine_kernel<D>, dim3((unsigned)(((long long)a.B * a.Hkv * rows + 1) / 2)),
+               dim3(kv::kCombineWarps * 64), 0, s, a,
                rows);
   }
   return launch_status();
@@ -184,9 +188,17 @@ int hbl_kv_attention(const hbl_bf16* Q, int T, int Hq, int Hkv, int D, long long
                        reinterpret_cast<long long*>(w + L.prefix), reinterpret_cast<float*>(w + L.ml),
                        reinterpret_cast<float*>(w + L.o), scale * kv::kLog2e, T, Hq, Hkv, Hq / Hkv, B, max_pages,
                        ilog2(page), num_pages, causal, window,
-                       std::min(d->sm_count, kv::kMaxAttnCtas), std::max(kFewRows, Hq / Hkv),
-                       (int)std::min<long long>((long long)(max_q ? max_q : T) * (Hq / Hkv), 0x7fffffffll), 0};
+                       std::min(kv::kAttnCtas * d->sm_count, kv::kMaxAttnCtas), std::max(kFewRows, Hq / Hkv),
+                       (int)std::min<long long>((long long)(max_q ? max_q : T) * (Hq / Hkv), 0x7fffffffll), 0, 0};
   a.tile_rows = std::min(a.most_rows, a.few_rows) <= 8 ? 8 : 16;
+  // Few enough keys for one CTA to be through with them before a second kernel could have joined the parts: each item
+  // is left whole (at most kWholeCtas of them, so that the grid stays a few waves).
+  const long long most_kv = std::min<long long>(max_kv ? max_kv : 1ll << 40, (long long)max_pages * page);
+  const int row_tiles = (std::min(a.most_rows, a.few_rows) + a.tile_rows - 1) / a.tile_rows;
+  if (most_kv <= kWholeKeys && (long long)B * Hkv * row_tiles <= kWholeCtas) {
+    a.row_tiles = row_tiles;
+    a.ctas = B * Hkv * row_tiles;
+  }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return D == 64 ? launch_kv_attention<64>(a, s) : launch_kv_attention<128>(a, s);
 }

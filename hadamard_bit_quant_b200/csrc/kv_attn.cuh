@@ -6,8 +6,8 @@
 //
 // The bound is the cache read: D bytes of keys and D of values for each token and head. The kernel is a stream over
 // tiles of 32 tokens:
-//   * one CTA per SM, each with an equal share of all tiles of all requests and heads (the long axis is
-//     split wherever the share ends), tiles dealt to 12 warps in turn;
+//   * two CTAs per SM, each with an equal share of all tiles of all requests and heads (the long axis is
+//     split wherever the share ends), tiles dealt to 6 warps in turn;
 //   * each warp has a ring of its own in shared memory, filled with 16-byte cp.async, and its own reference
 //     maximum, sum and output in registers: no barrier while it streams. The next run's first tiles are fetched before
 //     the warps' results of this one are added up;
@@ -28,12 +28,13 @@
 namespace hbl {
 namespace kv {
 
-constexpr int kAttnWarps = 12;
+constexpr int kAttnWarps = 6;
+constexpr int kAttnCtas = 2;          // blocks of an SM
 constexpr int kAttnTile = 32;         // tokens of a warp's tile
 constexpr int kAttnRows = 16;         // most query rows of a tile
 constexpr float kLag = 8.f;           // log2 of how far a tile may outgrow the reference maximum
 constexpr float kSlack = 16.f;        // and a value scale the reference scale
-constexpr int kMaxAttnCtas = 256;     // workspace is laid out for this many
+constexpr int kMaxAttnCtas = 320;     // workspace is laid out for this many
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -57,6 +58,7 @@ struct AttnArgs {
   int few_rows;                       // requests with more rows per key/value head than this go to kv_prefill_kernel
   int most_rows;                      // and those with more than this break the caller's bound
   int tile_rows;                      // query rows that kv_attn_kernel takes at a time: 8 or 16
+  int row_tiles;                      // > 0: one CTA for each request, head and of so many row tiles, nothing is split
 };
 
 // A request as the kernels see it: whatever the arrays hold, rows stay inside Q and keys inside the table.
@@ -82,6 +84,11 @@ HBL_DEVINL bool prefill_request(const AttnArgs& a, const Request& r) {
   return !r.few && (long long)r.q * a.group <= a.most_rows;
 }
 HBL_DEVINL long long tiles_of(const AttnArgs& a, const Request& r) { return (long long)r.tiles * r.rt * a.Hkv; }
+
+// Rows beyond the caller's bound belong to no kernel that was launched for them.
+HBL_DEVINL void check_bound(const AttnArgs& a, const Request& r) {
+  if ((long long)r.q * a.group > a.most_rows) set_device_error(HBL_ERR_INVALID_ARG);
+}
 
 HBL_DEVINL void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
@@ -179,7 +186,7 @@ struct Run {
 };
 
 template <int D, int NT>   // NT: column tiles of 8 query rows
-__global__ void __launch_bounds__(kAttnWarps * 32, 1) kv_attn_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kAttnWarps * 32, kAttnCtas) kv_attn_kernel(const AttnArgs a) {
   using C = AttnCfg<D>;
   constexpr int NK = D / 16;          // k-steps of the score product
   constexpr int NJ = D / 16;          // row tiles of the output product
@@ -191,57 +198,79 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) kv_attn_kernel(const AttnA
   const int g = lane >> 2, t4 = lane & 3;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
 
-  // this CTA's share [w0, w1) of all tiles, and the request in which it begins
-  const int per = (a.B + blockDim.x - 1) / blockDim.x;
-  const int b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
-  long long sum = 0;
-  for (int b = b0; b < b1; ++b) sum += tiles_of(a, request_of(a, b));
-  long long ex = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, ex, o);
-    if (lane >= o) ex += y;
-  }
-  if (lane == 31) sh[warp] = ex;
-  __syncthreads();
-  long long total = 0, before = 0;
-#pragma unroll
-  for (int i = 0; i < kAttnWarps; ++i) {
-    if (i < warp) before += sh[i];
-    total += sh[i];
-  }
-  ex += before - sum;
-  if (blockIdx.x == 0) {
-    long long x = ex;
-    for (int b = b0; b < b1; ++b) {
-      a.prefix[b] = x;
-      x += tiles_of(a, request_of(a, b));
+  Run run;
+  long long at, left;                 // tile within the request, over (head, row tile, tile); tiles of this CTA to go
+  if (a.row_tiles > 0) {
+    const int rt = (int)(blockIdx.x % a.row_tiles), i = (int)(blockIdx.x / a.row_tiles), h = i % a.Hkv;
+    run.b = i / a.Hkv;
+    run.rq = request_of(a, run.b);
+    if (rt == 0 && h == 0 && threadIdx.x == 0) check_bound(a, run.rq);
+    if (!run.rq.few || rt >= run.rq.rt) return;
+    if (run.rq.tiles == 0) {          // no key at all
+      const int row_lo = rt * 8 * NT, rows = min(8 * NT, run.rq.q * a.group - row_lo);
+      for (int k = threadIdx.x; k < rows * (D / 8); k += blockDim.x) {
+        const int r = row_lo + k / (D / 8);
+        const size_t out = (size_t)(run.rq.row0 + r / a.group) * a.Hq + (size_t)(h * a.group + r % a.group);
+        reinterpret_cast<uint4*>(a.O + out * D)[k % (D / 8)] = make_uint4(0, 0, 0, 0);
+        if (a.lse && k % (D / 8) == 0) a.lse[out] = -INFINITY;
+      }
+      return;
     }
-    if (threadIdx.x == 0) a.prefix[a.B] = total;
-  }
-  const long long n = min(total, (long long)a.ctas);      // no CTA before this one is without a tile
-  if (blockIdx.x >= n) return;
-  const long long w0 = total * blockIdx.x / n, w1 = total * (blockIdx.x + 1) / n;
-  if (ex <= w0 && w0 < ex + sum) {
-    long long x = ex;
-    for (int b = b0; b < b1; ++b) {
-      const long long tiles = tiles_of(a, request_of(a, b));
-      if (w0 < x + tiles) { s_b = b; s_off = w0 - x; break; }
-      x += tiles;
+    at = ((long long)h * run.rq.rt + rt) * run.rq.tiles;
+    left = run.rq.tiles;
+  } else {
+    // this CTA's share [w0, w1) of all tiles, and the request in which it begins
+    const int per = (a.B + blockDim.x - 1) / blockDim.x;
+    const int b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) sum += tiles_of(a, request_of(a, b));
+    long long ex = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, ex, o);
+      if (lane >= o) ex += y;
     }
+    if (lane == 31) sh[warp] = ex;
+    __syncthreads();
+    long long total = 0, before = 0;
+#pragma unroll
+    for (int i = 0; i < kAttnWarps; ++i) {
+      if (i < warp) before += sh[i];
+      total += sh[i];
+    }
+    ex += before - sum;
+    if (blockIdx.x == 0) {
+      long long x = ex;
+      for (int b = b0; b < b1; ++b) {
+        a.prefix[b] = x;
+        x += tiles_of(a, request_of(a, b));
+      }
+      if (threadIdx.x == 0) a.prefix[a.B] = total;
+    }
+    const long long n = min(total, (long long)a.ctas);      // no CTA before this one is without a tile
+    if (blockIdx.x >= n) return;
+    const long long w0 = total * blockIdx.x / n, w1 = total * (blockIdx.x + 1) / n;
+    if (ex <= w0 && w0 < ex + sum) {
+      long long x = ex;
+      for (int b = b0; b < b1; ++b) {
+        const long long tiles = tiles_of(a, request_of(a, b));
+        if (w0 < x + tiles) { s_b = b; s_off = w0 - x; break; }
+        x += tiles;
+      }
+    }
+    __syncthreads();
+    run.b = s_b;
+    run.rq = request_of(a, run.b);
+    at = s_off;
+    left = w1 - w0;
   }
-  __syncthreads();
 
   uint8_t* ring = smem + warp * (C::kStages * C::kStageBytes);
   const uint32_t ring_u = (uint32_t)__cvta_generic_to_shared(ring);
   float* merge = reinterpret_cast<float*>(smem + C::kRing);                        // [warp][4][D], chunks permuted
   float2* merge_ml = reinterpret_cast<float2*>(smem + C::kRing + C::kMerge);       // [warp][8 NT]
 
-  // The run at tile `at` of request r.b, with `left` tiles of the CTA's share to go.
-  Run run;
-  run.b = s_b;
-  run.rq = request_of(a, run.b);
-  long long at = s_off, left = w1 - w0;
+  // The run that begins at tile `at` of request r.b.
   auto open = [&](Run& r) {
     while (at >= tiles_of(a, r.rq)) {   // the next request with any tiles
       at = 0;
@@ -600,48 +629,78 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) kv_attn_kernel(const AttnA
   }
 }
 
-// Joins the parts of rows whose keys were split between CTAs, and writes the rows that see nothing at all.
-// One warp per (request, key/value head, row), `rows` of them for each request and head.
+// Joins the parts of rows whose keys were split between CTAs, and writes the rows that see nothing at all. Four
+// warps for each (request, key/value head, row), `rows` of them for each request and head; warp k takes every
+// fourth part, and what it has to read of them depends on nothing but their numbers.
+constexpr int kCombineWarps = 4;
+
 template <int D>
-__global__ void __launch_bounds__(256) kv_combine_kernel(const AttnArgs a, const int rows) {
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const int lane = threadIdx.x & 31;
-  const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lo = (int)(i / ((long long)rows * a.Hkv)), r = (int)(i % rows), h = (int)(i / rows % a.Hkv);
-  if (lo >= a.B) return;
-  const Request rq = request_of(a, lo);
-  if (r == 0 && h == 0 && lane == 0 && (long long)rq.q * a.group > a.most_rows) set_device_error(HBL_ERR_INVALID_ARG);
-  if (!rq.few || r >= rq.q * a.group) return;
-  const int rt = r / a.tile_rows;
-  const size_t row = (size_t)(rq.row0 + r / a.group) * a.Hq + (size_t)(h * a.group + r % a.group);
-  float M = -INFINITY, L = 0.f;
+__global__ void __launch_bounds__(kCombineWarps * 64) kv_combine_kernel(const AttnArgs a, const int rows) {
   constexpr int V = D / 32;                                 // channels of a lane
-  float acc[V] = {};
-  if (rq.tiles > 0) {
-    const long long total = a.prefix[a.B];
-    const long long x0 = a.prefix[lo] + (long long)(h * rq.rt + rt) * rq.tiles, x1 = x0 + rq.tiles - 1;
-    // CTA c holds the tiles from total * c / n on
-    const long long n = min(total, (long long)a.ctas);
-    const int c0 = (int)(((x0 + 1) * n + total - 1) / total) - 1;
-    const int c1 = (int)(((x1 + 1) * n + total - 1) / total) - 1;
-    if (c0 == c1) return;                                   // written by that CTA
-    for (int c = c0; c <= c1; ++c) {
-      const bool begins = c > c0 || total * c / n == x0;   // the CTA's first item, or its last
-      const size_t slot = ((size_t)c * 2 + (begins ? 0 : 1)) * kAttnRows + r % a.tile_rows;
-      const float m = a.part_ml[2 * slot], l = a.part_ml[2 * slot + 1];
-      const float mn = fmaxf(M, m), mu = mn == -INFINITY ? 0.f : mn;
-      const float f0 = exp2_fast(M - mu), f1 = exp2_fast(m - mu);
-      M = mn;
-      L = L * f0 + l * f1;
+  __shared__ float s_acc[2][kCombineWarps][D];
+  __shared__ float2 s_ml[2][kCombineWarps];
+  const int lane = threadIdx.x & 31, k = (threadIdx.x >> 5) % kCombineWarps, half = threadIdx.x / (32 * kCombineWarps);
+  const long long i = (long long)blockIdx.x * 2 + half;
+  const int b = (int)(i / ((long long)rows * a.Hkv)), r = (int)(i % rows), h = (int)(i / rows % a.Hkv);
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  bool mine = b < a.B;                                      // the row is there and is to be written here
+  size_t row = 0;
+  float M = -INFINITY, L = 0.f, acc[V] = {};
+  if (mine) {
+    const Request rq = request_of(a, b);
+    if (r == 0 && h == 0 && k == 0 && lane == 0) check_bound(a, rq);
+    mine = rq.few && r < rq.q * a.group;
+    row = (size_t)(rq.row0 + r / a.group) * a.Hq + (size_t)(h * a.group + r % a.group);
+    if (mine && rq.tiles > 0) {
+      const long long total = a.prefix[a.B], n = min(total, (long long)a.ctas);
+      const long long x0 = a.prefix[b] + (long long)(h * rq.rt + r / a.tile_rows) * rq.tiles, x1 = x0 + rq.tiles - 1;
+      // CTA c holds the tiles from total * c / n on
+      const int c0 = (int)(((x0 + 1) * n + total - 1) / total) - 1;
+      const int c1 = (int)(((x1 + 1) * n + total - 1) / total) - 1;
+      mine = c0 < c1;                                       // else written by that CTA
+      if (mine) {
+        // the first part is its CTA's last item, unless the CTA begins with it; every other one is its CTA's first
+        const int tail = total * c0 / n != x0;
+        for (int c = c0 + k; c <= c1; c += kCombineWarps) {
+          const size_t slot = ((size_t)c * 2 + (c == c0 ? tail : 0)) * kAttnRows + r % a.tile_rows;
+          const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * slot);
+          float v[V];
+          if constexpr (V == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(a.part_o + slot * D + V * lane);
+          else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(a.part_o + slot * D + V * lane);
+          const float mn = fmaxf(M, ml.x), mu = mn == -INFINITY ? 0.f : mn;
+          const float f0 = exp2_fast(M - mu), f1 = exp2_fast(ml.x - mu);
+          M = mn;
+          L = L * f0 + ml.y * f1;
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = acc[i] * f0 + a.part_o[slot * D + V * lane + i] * f1;
+          for (int e = 0; e < V; ++e) acc[e] = acc[e] * f0 + v[e] * f1;
+        }
+      }
     }
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) s_acc[half][k][V * lane + e] = acc[e];
+  if (lane == 0) s_ml[half][k] = make_float2(M, L);
+  __syncthreads();
+  if (!mine || k != 0) return;
+  M = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kCombineWarps; ++w) M = fmaxf(M, s_ml[half][w].x);
+  const float mu = M == -INFINITY ? 0.f : M;
+  L = 0.f;
+#pragma unroll
+  for (int e = 0; e < V; ++e) acc[e] = 0.f;
+#pragma unroll
+  for (int w = 0; w < kCombineWarps; ++w) {
+    const float f = exp2_fast(s_ml[half][w].x - mu);
+    L += s_ml[half][w].y * f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] += s_acc[half][w][V * lane + e] * f;
   }
   const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
 #pragma unroll
-  for (int i = 0; i < V; i += 2)
-    *reinterpret_cast<uint32_t*>(a.O + row * D + V * lane + i) =
-        (uint32_t)float_to_bf16_bits(acc[i] * inv) | ((uint32_t)float_to_bf16_bits(acc[i + 1] * inv) << 16);
+  for (int e = 0; e < V; e += 2)
+    *reinterpret_cast<uint32_t*>(a.O + row * D + V * lane + e) =
+        (uint32_t)float_to_bf16_bits(acc[e] * inv) | ((uint32_t)float_to_bf16_bits(acc[e + 1] * inv) << 16);
   if (a.lse && lane == 0) a.lse[row] = L > 0.f || L != L ? M * kLn2 + logf(L) : -INFINITY;
 }
 

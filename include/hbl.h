@@ -354,8 +354,9 @@ size_t hbl_kv_attention_workspace_bytes(int B, int D);
  *             T). It decides which kernels are launched; the rows of a request
  *             with more are left as they were, which is recorded in the device
  *             error word.
- *   max_kv  : the most cached tokens likewise (0: max_pages * page). A hint:
- *             it changes no result.
+ *   max_kv  : the most cached tokens likewise (0: max_pages * page). A hint by
+ *             which kernels are chosen; with a wrong one the rows are right,
+ *             only slower.
  *   scale   : finite, > 0; multiplies the scores.
  *   causal  : 1: row i of q sees the keys up to position kv - q + i; 0: all.
  *   window  : > 0 (with causal only): and of those the last `window`. 0: none.
