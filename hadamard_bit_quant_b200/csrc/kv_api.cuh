@@ -69,10 +69,11 @@ int launch_kv_attention(const kv::AttnArgs& a, cudaStream_t s) {
   }
   if (a.row_tiles == 0) {
     ProfScope ps("kv_combine", s);
+    // few rows have many parts, many rows have few
     const int rows = std::min(a.few_rows, a.most_rows);
-    launch_pdl(kv::kv_combine_kernel<D>, dim3((unsigned)(((long long)a.B * a.Hkv * rows + 1) / 2)),
-               dim3(kv::kCombineWarps * 64), 0, s, a,
-               rows);
+    const long long all = (long long)a.B * a.Hkv * rows;
+    if (all <= 1024) launch_pdl(kv::kv_combine_kernel<D, 4>, dim3((unsigned)((all + 1) / 2)), dim3(256), 0, s, a, rows);
+    else launch_pdl(kv::kv_combine_kernel<D, 1>, dim3((unsigned)((all + 7) / 8)), dim3(256), 0, s, a, rows);
   }
   return launch_status();
 }
@@ -123,12 +124,15 @@ int hbl_kv_append(const hbl_bf16* K, const hbl_bf16* V, int T, int Hkv, int D, l
   DeviceState* d = nullptr;
   if ((st = ensure_device(&d))) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const kv::AppendArgs a{{K, V}, {k_stride, v_stride}, {kcodes, vcodes}, {kscale, vscale}, slots, T, Hkv,
-                         ilog2(page), num_pages};
-  const dim3 grid((T + 7) / 8, Hkv, 2);
+  const kv::AppendArgs a{K, V, k_stride, v_stride, kcodes, vcodes, kscale, vscale, slots, T, Hkv, ilog2(page), num_pages};
+  // Spans of a page (64 tokens at least) when there are many tokens, so that a run fills a block; shorter ones when the
+  // grid would else be smaller than two blocks for each place on the GPU.
+  int span = std::max(page, 64);
+  while (span > 8 && (long long)((T + span - 1) / span) * Hkv * 2 < 16ll * d->sm_count) span /= 2;
+  const dim3 grid((T + span - 1) / span, Hkv, 2);
   ProfScope ps("kv_append", s);
-  if (D == 64) launch_pdl(kv::kv_append_kernel<64>, grid, dim3(256), 0, s, a);
-  else launch_pdl(kv::kv_append_kernel<128>, grid, dim3(256), 0, s, a);
+  if (D == 64) launch_pdl(kv::kv_append_kernel<64>, grid, dim3(kv::kAppendThreads), 0, s, a, span);
+  else launch_pdl(kv::kv_append_kernel<128>, grid, dim3(kv::kAppendThreads), 0, s, a, span);
   return launch_status();
 }
 
@@ -144,8 +148,9 @@ int hbl_kv_read(const int32_t* slots, int T, int Hkv, int D, int page, int num_p
   DeviceState* d = nullptr;
   if ((st = ensure_device(&d))) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const kv::ReadArgs a{{kcodes, vcodes}, {kscale, vscale}, {K, V}, slots, T, Hkv, ilog2(page), num_pages};
-  const dim3 grid((unsigned)(((long long)T * Hkv * (D / 8) + 255) / 256), 2);
+  const kv::ReadArgs a{kcodes, vcodes, kscale, vscale, K, V, slots, T, Hkv, ilog2(page), num_pages};
+  const long long vectors = (long long)T * Hkv * (D / 8), per = 256 * kv::kReadItems;
+  const dim3 grid((unsigned)((vectors + per - 1) / per), 2);
   ProfScope ps("kv_read", s);
   if (D == 64) launch_pdl(kv::kv_read_kernel<64>, grid, dim3(256), 0, s, a);
   else launch_pdl(kv::kv_read_kernel<128>, grid, dim3(256), 0, s, a);

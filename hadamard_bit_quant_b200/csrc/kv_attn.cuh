@@ -629,18 +629,17 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kAttnCtas) kv_attn_kernel(con
   }
 }
 
-// Joins the parts of rows whose keys were split between CTAs, and writes the rows that see nothing at all. Four
-// warps for each (request, key/value head, row), `rows` of them for each request and head; warp k takes every
-// fourth part, and what it has to read of them depends on nothing but their numbers.
-constexpr int kCombineWarps = 4;
-
-template <int D>
-__global__ void __launch_bounds__(kCombineWarps * 64) kv_combine_kernel(const AttnArgs a, const int rows) {
+// Joins the parts of rows whose keys were split between CTAs, and writes the rows that see nothing at all. KW
+// warps for each (request, key/value head, row), `rows` of them for each request and head; each takes every
+// KW-th part, and what it has to read of them depends on nothing but their numbers.
+template <int D, int KW>
+__global__ void __launch_bounds__(256) kv_combine_kernel(const AttnArgs a, const int rows) {
   constexpr int V = D / 32;                                 // channels of a lane
-  __shared__ float s_acc[2][kCombineWarps][D];
-  __shared__ float2 s_ml[2][kCombineWarps];
-  const int lane = threadIdx.x & 31, k = (threadIdx.x >> 5) % kCombineWarps, half = threadIdx.x / (32 * kCombineWarps);
-  const long long i = (long long)blockIdx.x * 2 + half;
+  constexpr int kPer = 8 / KW;                              // rows of a block
+  __shared__ float s_acc[kPer][KW][D];
+  __shared__ float2 s_ml[kPer][KW];
+  const int lane = threadIdx.x & 31, k = (threadIdx.x >> 5) % KW, half = threadIdx.x / (32 * KW);
+  const long long i = (long long)blockIdx.x * kPer + half;
   const int b = (int)(i / ((long long)rows * a.Hkv)), r = (int)(i % rows), h = (int)(i / rows % a.Hkv);
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   bool mine = b < a.B;                                      // the row is there and is to be written here
@@ -661,7 +660,7 @@ __global__ void __launch_bounds__(kCombineWarps * 64) kv_combine_kernel(const At
       if (mine) {
         // the first part is its CTA's last item, unless the CTA begins with it; every other one is its CTA's first
         const int tail = total * c0 / n != x0;
-        for (int c = c0 + k; c <= c1; c += kCombineWarps) {
+        for (int c = c0 + k; c <= c1; c += KW) {
           const size_t slot = ((size_t)c * 2 + (c == c0 ? tail : 0)) * kAttnRows + r % a.tile_rows;
           const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * slot);
           float v[V];
@@ -677,25 +676,27 @@ __global__ void __launch_bounds__(kCombineWarps * 64) kv_combine_kernel(const At
       }
     }
   }
+  if constexpr (KW > 1) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) s_acc[half][k][V * lane + e] = acc[e];
-  if (lane == 0) s_ml[half][k] = make_float2(M, L);
-  __syncthreads();
-  if (!mine || k != 0) return;
-  M = -INFINITY;
+    for (int e = 0; e < V; ++e) s_acc[half][k][V * lane + e] = acc[e];
+    if (lane == 0) s_ml[half][k] = make_float2(M, L);
+    __syncthreads();
+    M = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < kCombineWarps; ++w) M = fmaxf(M, s_ml[half][w].x);
-  const float mu = M == -INFINITY ? 0.f : M;
-  L = 0.f;
+    for (int w = 0; w < KW; ++w) M = fmaxf(M, s_ml[half][w].x);
+    const float mu = M == -INFINITY ? 0.f : M;
+    L = 0.f;
 #pragma unroll
-  for (int e = 0; e < V; ++e) acc[e] = 0.f;
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
 #pragma unroll
-  for (int w = 0; w < kCombineWarps; ++w) {
-    const float f = exp2_fast(s_ml[half][w].x - mu);
-    L += s_ml[half][w].y * f;
+    for (int w = 0; w < KW; ++w) {
+      const float f = exp2_fast(s_ml[half][w].x - mu);
+      L += s_ml[half][w].y * f;
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] += s_acc[half][w][V * lane + e] * f;
+      for (int e = 0; e < V; ++e) acc[e] += s_acc[half][w][V * lane + e] * f;
+    }
   }
+  if (!mine || k != 0) return;
   const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
 #pragma unroll
   for (int e = 0; e < V; e += 2)

@@ -187,147 +187,258 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(PlanArgs a) {
 // Appending.
 // ---------------------------------------------------------------------------
 
-// rint(x / s), ties to even, of the exact quotient. r = rint(x * (1/s)) is within one of it; the remainder
-// x - r s is exact in fp32 (it is a multiple of half an ulp of s and not larger than s), so comparing it
-// with s / 2 decides.
-HBL_DEVINL float quotient(float x, float s, float inv) {
-  float r = rintf(__fmul_rn(x, inv));
-  const float d = __fmaf_rn(-r, s, x), h = 0.5f * s;
-  const bool odd = ((int)r) & 1;
-  if (fabsf(d) > h || (fabsf(d) == h && odd)) r += copysignf(1.f, d);
-  return r;
+// A code 128 + rint(x / s), ties to even, of the exact quotient, in the low byte of the result. t holds the
+// integer r nearest to x * (1/s) behind 1.5 * 2^23 + 128; r is within one of the answer. The remainder x - r s is exact in fp32
+// (it is a multiple of half an ulp of s and not larger than s), so comparing it with s / 2 decides; it is
+// hardly ever as large.
+HBL_DEVINL uint32_t code_of(float x, float s, float inv, float h) {
+  const float magic = 12583040.0f;
+  float t = __fmaf_rn(x, inv, magic);
+  const float d = __fmaf_rn(-__fsub_rn(t, magic), s, x);
+  if (fabsf(d) >= h) {
+    const bool odd = __float_as_uint(t) & 1u;               // 128 is even
+    if (fabsf(d) > h || odd) t = __fadd_rn(t, copysignf(1.f, d));
+  }
+  return __float_as_uint(t);
 }
 
-// A bf16 value as the cache takes it: there is no code for NaN (0 is stored) or infinity (the largest
+// Two bf16 values as the cache takes them: there is no code for NaN (0 is stored) or infinity (the largest
 // finite value is stored).
-HBL_DEVINL float finite(float x) {
-  const float big = __uint_as_float(0x7f7f0000u);   // largest finite bf16
-  return x != x ? 0.f : fminf(fmaxf(x, -big), big);
+HBL_DEVINL uint32_t finite2(uint32_t w) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 16) {
+    const uint32_t v = (w >> e) & 0x7fffu;
+    if (v > 0x7f80u) w &= ~(0xffffu << e);
+    else if (v == 0x7f80u) w -= 1u << e;
+  }
+  return w;
 }
-HBL_DEVINL float lo_bf16(uint32_t w) { return finite(__uint_as_float(w << 16)); }
-HBL_DEVINL float hi_bf16(uint32_t w) { return finite(__uint_as_float(w & 0xffff0000u)); }
+HBL_DEVINL uint32_t max_abs2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
+
+// The 8 codes of 8 bf16 values.
+HBL_DEVINL uint2 codes8(const uint4& x, float s, float inv, float h) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t c[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    c[2 * k] = code_of(__uint_as_float(w[k] << 16), s, inv, h);
+    c[2 * k + 1] = code_of(__uint_as_float(w[k] & 0xffff0000u), s, inv, h);
+  }
+  return make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
+}
 
 struct AppendArgs {
-  const uint16_t* x[2];               // keys, values
-  long long stride[2];                // elements from token to token
-  uint8_t* codes[2];
-  float* scale[2];
+  const uint16_t *k, *v;              // keys, values
+  long long kstride, vstride;         // elements from token to token
+  uint8_t *kcodes, *vcodes;
+  float *kscale, *vscale;
   const int32_t* slots;
   int T, H, page_log2, num_pages;
 };
 
-// One warp for each (first token of a run, head, keys or values). A run is a row of tokens in consecutive
-// slots of one page: the warp finds the run's absmax, raises the block's scale to it if it must (rescaling
-// the codes that the block held before the run), and writes the run's codes.
+constexpr int kAppendThreads = 256;
+constexpr int kAppendSpan = 128;      // most tokens of a block's span
+constexpr int kAppendHeld = 8;        // 16-byte vectors that a thread holds
+
+// The tokens of one run, handled by `NT` threads (a warp or the block) of which this is number `tid`.
+// `reduce` gives all of them the largest of their values. What fits in registers is read once.
+template <int D, int NT, typename Reduce>
+HBL_DEVINL void append_run(const uint16_t* x, long long stride, int n, int off, int P, uint8_t* codes, float* scale, int tid,
+                           Reduce reduce) {
+  constexpr int VPT = D / 8;          // vectors of a token
+  const int total = n * VPT;
+  const float held = off > 0 ? *scale : 0.f;
+  const float before = held >= 0.f && held <= 3.4e38f ? held : 0.f;
+  auto vec = [&](int i) { return __ldg(reinterpret_cast<const uint4*>(x + (size_t)(i / VPT) * (size_t)stride) + i % VPT); };
+  uint4 v[kAppendHeld];
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < kAppendHeld; ++k) {
+    v[k] = tid + k * NT < total ? vec(tid + k * NT) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int k = 0; k < kAppendHeld; ++k) m = max_abs2(max_abs2(max_abs2(max_abs2(m, v[k].x), v[k].y), v[k].z), v[k].w);
+  for (int i = tid + kAppendHeld * NT; i < total; i += NT) {
+    const uint4 w = vec(i);
+    m = max_abs2(max_abs2(max_abs2(max_abs2(m, w.x), w.y), w.z), w.w);
+  }
+  uint32_t top = reduce(max(m & 0xffffu, m >> 16));
+  const bool odd = top >= 0x7f80u;    // NaN or infinity among them: once more, with what is stored for those
+  if (odd) {
+    m = 0;
+    for (int i = tid; i < total; i += NT) {
+      const uint4 w = vec(i);
+      m = max_abs2(max_abs2(max_abs2(max_abs2(m, finite2(w.x)), finite2(w.y)), finite2(w.z)), finite2(w.w));
+    }
+    top = reduce(max(m & 0xffffu, m >> 16));
+#pragma unroll
+    for (int k = 0; k < kAppendHeld; ++k)
+      v[k] = make_uint4(finite2(v[k].x), finite2(v[k].y), finite2(v[k].z), finite2(v[k].w));
+  }
+  const float s = fmaxf(before, fmaxf(__fdiv_rn(__uint_as_float(top << 16), 127.f), kScaleFloor));
+  const float inv = __frcp_rn(s), h = 0.5f * s;
+  if (s != before) {                  // what the block held before the run
+    for (int i = tid; i < off * (D / 4); i += NT) {
+      const uint32_t w = reinterpret_cast<uint32_t*>(codes)[i];
+      uint32_t c[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        c[k] = code_of(__fmul_rn((float)((int)((w >> (8 * k)) & 255u) - kZero), before), s, inv, h);
+      reinterpret_cast<uint32_t*>(codes)[i] =
+          __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+    }
+  }
+  uint2* dst = reinterpret_cast<uint2*>(codes + (size_t)off * D);
+#pragma unroll
+  for (int k = 0; k < kAppendHeld; ++k)
+    if (tid + k * NT < total) dst[tid + k * NT] = codes8(v[k], s, inv, h);
+  for (int i = tid + kAppendHeld * NT; i < total; i += NT) {
+    uint4 w = vec(i);
+    if (odd) w = make_uint4(finite2(w.x), finite2(w.y), finite2(w.z), finite2(w.w));
+    dst[i] = codes8(w, s, inv, h);
+  }
+  if (tid == 0) *scale = s;           // every thread has read it: it lies behind a reduction
+}
+
+// A run is a row of tokens in consecutive slots of one page. A block takes the runs that begin in its span of
+// tokens, for one head's keys or values: a single long one with all its threads, several (or a short one) with a
+// warp each. It finds the run's absmax, raises the block's scale to it if it must (rescaling the codes that the
+// block held before the run), and writes the run's codes; the values are read once, for both.
 template <int D>
-__global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
-  constexpr int LPT = D / 8;          // lanes of a token, 8 values each
-  constexpr int TPW = 32 / LPT;       // tokens side by side in a warp
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a, const int span) {
+  __shared__ unsigned s_heads[kAppendSpan / 32];
+  __shared__ uint32_t s_max[2][kAppendThreads / 32];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const int lane = threadIdx.x & 31, h = blockIdx.y, kind = blockIdx.z;
-  const int t0 = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (t0 >= a.T) return;
-  const int P = 1 << a.page_log2;
-  const int slot = a.slots[t0];
-  if (slot < 0) return;
-  if (slot >= (a.num_pages << a.page_log2)) {
-    if (lane == 0) set_device_error(HBL_ERR_INVALID_ARG);
-    return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
+  const bool keys = blockIdx.z == 0;
+  const int P = 1 << a.page_log2, t0 = blockIdx.x * span;
+  const uint32_t slots = (uint32_t)a.num_pages << a.page_log2;
+  if (threadIdx.x < kAppendSpan) {
+    const int t = t0 + (int)threadIdx.x;
+    bool head = false;
+    if ((int)threadIdx.x < span && t < a.T) {
+      const int slot = a.slots[t];
+      head = slot >= 0 && (uint32_t)slot < slots && ((slot & (P - 1)) == 0 || t == 0 || a.slots[t - 1] != slot - 1);
+      if (slot >= 0 && (uint32_t)slot >= slots) set_device_error(HBL_ERR_INVALID_ARG);
+    }
+    const unsigned b = __ballot_sync(0xffffffffu, head);
+    if (lane == 0) s_heads[warp] = b;
   }
-  const int off = slot & (P - 1);
-  if (t0 > 0 && off > 0 && a.slots[t0 - 1] == slot - 1) return;   // not the first of its run
-  int n = 1;
-  while (true) {
-    const int m = n + lane;
-    const bool in = off + m < P && t0 + m < a.T && a.slots[t0 + m] == slot + m;
-    const unsigned out = ~__ballot_sync(0xffffffffu, in);
-    if (out) { n += __ffs(out) - 1; break; }
-    n += 32;
-  }
-  const uint16_t* x = a.x[kind] + (size_t)t0 * (size_t)a.stride[kind] + (size_t)h * D + 8 * (lane % LPT);
-  float gamma = 0.f;
-  for (int i = lane / LPT; i < n; i += TPW) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(x + (size_t)i * (size_t)a.stride[kind]));
-    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+  __syncthreads();
+  int runs = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) gamma = fmaxf(gamma, fmaxf(fabsf(lo_bf16(ws[k])), fabsf(hi_bf16(ws[k]))));
-  }
-  gamma = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(gamma)));
-  const size_t block = (size_t)(slot >> a.page_log2) * a.H + h;
-  uint8_t* codes = a.codes[kind] + block * (size_t)P * D;
-  float before = off > 0 ? a.scale[kind][block] : 0.f;
-  if (!(before >= 0.f && before <= 3.4e38f)) before = 0.f;
-  const float s = fmaxf(before, fmaxf(__fdiv_rn(gamma, 127.f), kScaleFloor));
-  const float inv = __frcp_rn(s);
-  if (off > 0 && s != before) {
-    for (int i = lane; i < off * (D / 4); i += 32) {
-      uint32_t w = reinterpret_cast<uint32_t*>(codes)[i], o = 0;
+  for (int i = 0; i < kAppendSpan / 32; ++i) runs += __popc(s_heads[i]);
+  if (runs == 0) return;
+  const uint16_t* x = keys ? a.k : a.v;
+  const long long stride = keys ? a.kstride : a.vstride;
+  // token, slot and length of the i-th run (by a whole warp)
+  auto run_of = [&](int i, int* slot, int* n) {
+    int w = 0;
+    while (i >= __popc(s_heads[w])) i -= __popc(s_heads[w++]);
+    const int t = t0 + 32 * w + (int)__fns(s_heads[w], 0, i + 1);
+    *slot = a.slots[t];
+    const int room = min(P - (*slot & (P - 1)), a.T - t);
+    *n = 1;
+    while (true) {
+      const bool in = *n + lane < room && a.slots[t + *n + lane] == *slot + *n + lane;
+      const unsigned out = ~__ballot_sync(0xffffffffu, in);
+      if (out) { *n += __ffs(out) - 1; break; }
+      *n += 32;
+    }
+    return t;
+  };
+  auto codes_at = [&](int slot) {
+    return (keys ? a.kcodes : a.vcodes) + (((size_t)(slot >> a.page_log2) * a.H + h) << a.page_log2) * D;
+  };
+  auto scale_at = [&](int slot) { return (keys ? a.kscale : a.vscale) + (size_t)(slot >> a.page_log2) * a.H + h; };
+  int slot, n;
+  if (runs == 1) {
+    const int t = run_of(0, &slot, &n);
+    if (n * (D / 8) > 4 * 32) {
+      int pass = 0;
+      append_run<D, kAppendThreads>(x + (size_t)t * (size_t)stride + (size_t)h * D, stride, n, slot & (P - 1), P, codes_at(slot),
+                                    scale_at(slot), threadIdx.x, [&](uint32_t m) {
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0) s_max[pass][warp] = m;
+        __syncthreads();
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float v = __fmul_rn((float)((int)((w >> (8 * k)) & 255u) - kZero), before);
-        o |= (uint32_t)((int)quotient(v, s, inv) + kZero) << (8 * k);
-      }
-      reinterpret_cast<uint32_t*>(codes)[i] = o;
+        for (int i = 0; i < kAppendThreads / 32; ++i) m = max(m, s_max[pass][i]);
+        pass ^= 1;
+        return m;
+      });
+      return;
     }
   }
-  for (int i = lane / LPT; i < n; i += TPW) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(x + (size_t)i * (size_t)a.stride[kind]));
-    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-    uint32_t o[2] = {0, 0};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t c0 = (uint32_t)((int)quotient(lo_bf16(ws[k]), s, inv) + kZero);
-      const uint32_t c1 = (uint32_t)((int)quotient(hi_bf16(ws[k]), s, inv) + kZero);
-      o[k >> 1] |= (c0 | (c1 << 8)) << (16 * (k & 1));
-    }
-    *reinterpret_cast<uint2*>(codes + (size_t)(off + i) * D + 8 * (lane % LPT)) = make_uint2(o[0], o[1]);
+  for (int i = warp; i < runs; i += kAppendThreads / 32) {
+    const int t = run_of(i, &slot, &n);
+    append_run<D, 32>(x + (size_t)t * (size_t)stride + (size_t)h * D, stride, n, slot & (P - 1), P, codes_at(slot), scale_at(slot),
+                      lane, [&](uint32_t m) { return __reduce_max_sync(0xffffffffu, m); });
   }
-  __syncwarp();
-  if (lane == 0) a.scale[kind][block] = s;
 }
 
 // ---------------------------------------------------------------------------
 // Reading back.
 // ---------------------------------------------------------------------------
 struct ReadArgs {
-  const uint8_t* codes[2];
-  const float* scale[2];
-  uint16_t* out[2];                   // T x H x D; either may be null
+  const uint8_t *kcodes, *vcodes;
+  const float *kscale, *vscale;
+  uint16_t *k, *v;                    // T x H x D; either may be null
   const int32_t* slots;
   int T, H, page_log2, num_pages;
 };
 
-// Eight values a thread: one 8-byte load of codes, one 16-byte store. bf16((u - 128) * s), the product
-// rounded to fp32 first.
+constexpr int kReadItems = 4;         // vectors of 8 values of a thread
+
+// bf16((u - 128) * s), the product rounded to fp32 first. A thread's four 8-byte loads of codes are all
+// issued before the first is used.
 template <int D>
-__global__ void __launch_bounds__(256) kv_read_kernel(ReadArgs a) {
+__global__ void __launch_bounds__(256) kv_read_kernel(const ReadArgs a) {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const int kind = blockIdx.y;
-  if (!a.out[kind]) return;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  const long long row = i / (D / 8);
-  if (row >= (long long)a.T * a.H) return;
-  const int t = (int)(row / a.H), h = (int)(row % a.H), c = (int)(i % (D / 8)) * 8;
-  const int slot = a.slots[t];
-  uint4 o = make_uint4(0, 0, 0, 0);
-  if (slot >= (a.num_pages << a.page_log2)) {
-    set_device_error(HBL_ERR_INVALID_ARG);
-  } else if (slot >= 0) {
-    const size_t block = (size_t)(slot >> a.page_log2) * a.H + h;
-    const int off = slot & ((1 << a.page_log2) - 1);
-    const uint2 w = *reinterpret_cast<const uint2*>(a.codes[kind] + ((block << a.page_log2) + off) * D + c);
-    const float s = a.scale[kind][block];
+  const bool keys = blockIdx.y == 0;
+  uint16_t* out = keys ? a.k : a.v;
+  if (!out) return;
+  const uint8_t* codes = keys ? a.kcodes : a.vcodes;
+  const float* scale = keys ? a.kscale : a.vscale;
+  const uint32_t rows = (uint32_t)a.T * (uint32_t)a.H;
+  const uint32_t slots = (uint32_t)a.num_pages << a.page_log2, pmask = (1u << a.page_log2) - 1u;
+  const uint32_t row0 = (uint32_t)(blockIdx.x * (size_t)(256 * kReadItems / (D / 8))) + threadIdx.x / (D / 8);
+  const int c = 8 * (int)(threadIdx.x % (D / 8));
+  uint2 w[kReadItems];
+  float s[kReadItems];
+#pragma unroll
+  for (int i = 0; i < kReadItems; ++i) {
+    const uint32_t row = row0 + (uint32_t)(i * (256 / (D / 8)));
+    w[i] = make_uint2(0, 0);
+    s[i] = 0.f;
+    if (row < rows) {
+      const uint32_t t = row / (uint32_t)a.H, h = row - t * (uint32_t)a.H;
+      const int slot = a.slots[t];
+      if (slot >= 0 && (uint32_t)slot >= slots) {
+        set_device_error(HBL_ERR_INVALID_ARG);
+      } else if (slot >= 0) {
+        const size_t block = (size_t)((uint32_t)slot >> a.page_log2) * a.H + h;
+        w[i] = __ldg(reinterpret_cast<const uint2*>(codes + ((block << a.page_log2) + ((uint32_t)slot & pmask)) * D + c));
+        s[i] = __ldg(scale + block);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kReadItems; ++i) {
+    const uint32_t row = row0 + (uint32_t)(i * (256 / (D / 8)));
+    if (row >= rows) break;
     uint32_t r[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const uint32_t v = (k < 2 ? w.x : w.y) >> (16 * (k & 1));
-      const float lo = __fmul_rn((float)((int)(v & 255u) - kZero), s);
-      const float hi = __fmul_rn((float)((int)((v >> 8) & 255u) - kZero), s);
-      r[k] = (uint32_t)float_to_bf16_bits(lo) | ((uint32_t)float_to_bf16_bits(hi) << 16);
+      // a byte in the low bits of 2^23, minus 2^23 + 128: the value of the code, exactly
+      const uint32_t u = k < 2 ? w[i].x : w[i].y;
+      const float lo = __uint_as_float(__byte_perm(u, 0x4b000000u, k & 1 ? 0x7552 : 0x7550)) - 8388736.0f;
+      const float hi = __uint_as_float(__byte_perm(u, 0x4b000000u, k & 1 ? 0x7553 : 0x7551)) - 8388736.0f;
+      const __nv_bfloat162 p = __floats2bfloat162_rn(__fmul_rn(lo, s[i]), __fmul_rn(hi, s[i]));
+      r[k] = *reinterpret_cast<const uint32_t*>(&p);
     }
-    o = make_uint4(r[0], r[1], r[2], r[3]);
+    *reinterpret_cast<uint4*>(out + (size_t)row * D + c) = make_uint4(r[0], r[1], r[2], r[3]);
   }
-  *reinterpret_cast<uint4*>(a.out[kind] + row * D + c) = o;
 }
 
 }  // namespace kv

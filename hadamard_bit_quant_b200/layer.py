@@ -5,6 +5,7 @@ is in libhbl's kernels.
 """
 from __future__ import annotations
 
+from functools import lru_cache
 from typing import NamedTuple
 
 import torch
@@ -131,6 +132,11 @@ class KVPages:
         return out
 
 
+@lru_cache(maxsize=256)
+def _attention_bytes(requests: int, head_dim: int) -> int:
+    return hbl.hbl_kv_attention_workspace_bytes(requests, head_dim)
+
+
 class KVCache:
     """One layer's paged 8-bit key/value cache.
 
@@ -174,16 +180,14 @@ class KVCache:
         """The values in the given slots: (K, V), bf16 [T, kv_heads, head_dim]."""
         _index(slots)
         T = slots.numel()
-        K, V = (torch.empty(T, self.kv_heads, self.head_dim, dtype=torch.bfloat16, device=self.kcodes.device)
-                for _ in range(2))
+        K, V = self.kcodes.new_empty((2, T, self.kv_heads, self.head_dim), dtype=torch.bfloat16)
         hbl.hbl_kv_read(slots, T, self.kv_heads, self.head_dim, self.page, self.num_pages, self.kcodes, self.vcodes,
                         self.kscale, self.vscale, K, V, stream)
         return K, V
 
     def workspace(self, requests: int) -> torch.Tensor:
         """Workspace of ``attention`` for a batch of that many requests."""
-        return torch.empty(hbl.hbl_kv_attention_workspace_bytes(requests, self.head_dim), dtype=torch.uint8,
-                           device=self.kcodes.device)
+        return self.kcodes.new_empty(_attention_bytes(requests, self.head_dim))
 
     def attention(self, Q: torch.Tensor, cu_q: torch.Tensor, kv_lens: torch.Tensor, block_table: torch.Tensor,
                   max_q: int = 0, max_kv: int = 0, scale: float | None = None, causal: bool = True, window: int = 0,
@@ -200,10 +204,10 @@ class KVCache:
         B = kv_lens.numel()
         assert cu_q.numel() == B + 1 and block_table.dim() == 2 and block_table.shape[0] == B
         if out is None:
-            out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=Q.device)
+            out = Q.new_empty(T, Hq, D)
         assert out.shape == Q.shape and out.dtype == torch.bfloat16 and out.is_contiguous() and out.device == Q.device
         if lse is None and return_lse:
-            lse = torch.empty(T, Hq, dtype=torch.float32, device=Q.device)
+            lse = self.kscale.new_empty(T, Hq)
         assert lse is None or (lse.shape == (T, Hq) and lse.dtype == torch.float32 and lse.is_contiguous())
         if ws is None:
             ws = self.workspace(B)
