@@ -213,16 +213,30 @@ HBL_DEVINL uint32_t finite2(uint32_t w) {
   }
   return w;
 }
-HBL_DEVINL uint32_t max_abs2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
+// Larger magnitudes of two pairs of bf16 values; NaN is the largest of all.
+HBL_DEVINL uint32_t max_abs2(uint32_t m, uint32_t w) {
+  const __nv_bfloat162 x = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&m),
+                                       __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)));
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
 
-// The 8 codes of 8 bf16 values.
+// The 8 codes of 8 bf16 values: code_of's first step for each, and its second only if any of them needs it.
 HBL_DEVINL uint2 codes8(const uint4& x, float s, float inv, float h) {
+  const float magic = 12583040.0f;
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t c[8];
+  bool close = false;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    c[2 * k] = code_of(__uint_as_float(w[k] << 16), s, inv, h);
-    c[2 * k + 1] = code_of(__uint_as_float(w[k] & 0xffff0000u), s, inv, h);
+  for (int k = 0; k < 8; ++k) {
+    const float v = __uint_as_float(k & 1 ? w[k >> 1] & 0xffff0000u : w[k >> 1] << 16);
+    const float t = __fmaf_rn(v, inv, magic);
+    close |= fabsf(__fmaf_rn(-__fsub_rn(t, magic), s, v)) >= h;
+    c[k] = __float_as_uint(t);
+  }
+  if (close) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      c[k] = code_of(__uint_as_float(k & 1 ? w[k >> 1] & 0xffff0000u : w[k >> 1] << 16), s, inv, h);
   }
   return make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
                     __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
@@ -238,7 +252,7 @@ struct AppendArgs {
 };
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendSpan = 128;      // most tokens of a block's span
+constexpr int kAppendSpan = 128;      // most tokens of a block's span; its last run may go on for a page
 constexpr int kAppendHeld = 8;        // 16-byte vectors that a thread holds
 
 // The tokens of one run, handled by `NT` threads (a warp or the block) of which this is number `tid`.
@@ -306,52 +320,59 @@ HBL_DEVINL void append_run(const uint16_t* x, long long stride, int n, int off, 
 // warp each. It finds the run's absmax, raises the block's scale to it if it must (rescaling the codes that the
 // block held before the run), and writes the run's codes; the values are read once, for both.
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a, const int span) {
-  __shared__ unsigned s_heads[kAppendSpan / 32];
-  __shared__ uint32_t s_max[2][kAppendThreads / 32];
+__global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const AppendArgs a, const int span) {
+  constexpr int kWords = kAppendThreads / 32;
+  __shared__ unsigned s_head[kWords], s_on[kWords];         // bit t: a run begins at token t0 + t; a run goes on there
+  __shared__ int s_slot[kAppendThreads];
+  __shared__ uint32_t s_max[2][kWords];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
   const bool keys = blockIdx.z == 0;
   const int P = 1 << a.page_log2, t0 = blockIdx.x * span;
   const uint32_t slots = (uint32_t)a.num_pages << a.page_log2;
-  if (threadIdx.x < kAppendSpan) {
+  {
     const int t = t0 + (int)threadIdx.x;
-    bool head = false;
-    if ((int)threadIdx.x < span && t < a.T) {
-      const int slot = a.slots[t];
-      head = slot >= 0 && (uint32_t)slot < slots && ((slot & (P - 1)) == 0 || t == 0 || a.slots[t - 1] != slot - 1);
-      if (slot >= 0 && (uint32_t)slot >= slots) set_device_error(HBL_ERR_INVALID_ARG);
+    const int now = t < a.T ? a.slots[t] : -1, last = t > 0 && t < a.T ? a.slots[t - 1] : -1;
+    const bool valid = now >= 0 && (uint32_t)now < slots;
+    const bool on = valid && (now & (P - 1)) != 0 && last == now - 1;
+    if (now >= 0 && !valid) set_device_error(HBL_ERR_INVALID_ARG);
+    s_slot[threadIdx.x] = now;
+    const unsigned goes_on = __ballot_sync(0xffffffffu, on);
+    const unsigned begins = __ballot_sync(0xffffffffu, valid && !on && (int)threadIdx.x < span);
+    if (lane == 0) {
+      s_head[warp] = begins;
+      s_on[warp] = goes_on;
     }
-    const unsigned b = __ballot_sync(0xffffffffu, head);
-    if (lane == 0) s_heads[warp] = b;
   }
   __syncthreads();
   int runs = 0;
 #pragma unroll
-  for (int i = 0; i < kAppendSpan / 32; ++i) runs += __popc(s_heads[i]);
+  for (int i = 0; i < kWords; ++i) runs += __popc(s_head[i]);
   if (runs == 0) return;
   const uint16_t* x = keys ? a.k : a.v;
   const long long stride = keys ? a.kstride : a.vstride;
-  // token, slot and length of the i-th run (by a whole warp)
+  // token, slot and length of the i-th run
   auto run_of = [&](int i, int* slot, int* n) {
     int w = 0;
-    while (i >= __popc(s_heads[w])) i -= __popc(s_heads[w++]);
-    const int t = t0 + 32 * w + (int)__fns(s_heads[w], 0, i + 1);
-    *slot = a.slots[t];
-    const int room = min(P - (*slot & (P - 1)), a.T - t);
-    *n = 1;
-    while (true) {
-      const bool in = *n + lane < room && a.slots[t + *n + lane] == *slot + *n + lane;
-      const unsigned out = ~__ballot_sync(0xffffffffu, in);
-      if (out) { *n += __ffs(out) - 1; break; }
-      *n += 32;
+    while (i >= __popc(s_head[w])) i -= __popc(s_head[w++]);
+    unsigned b = s_head[w];
+    for (; i > 0; --i) b &= b - 1;
+    const int t = 32 * w + __ffs(b) - 1;
+    *slot = s_slot[t];
+    int end = t + 1;
+    while (end < kAppendThreads) {
+      const unsigned stop = ~s_on[end >> 5] >> (end & 31);
+      if (stop) { end += __ffs(stop) - 1; break; }
+      end = (end | 31) + 1;
     }
-    return t;
+    *n = min(end, kAppendThreads) - t;
+    return t0 + t;
   };
   auto codes_at = [&](int slot) {
     return (keys ? a.kcodes : a.vcodes) + (((size_t)(slot >> a.page_log2) * a.H + h) << a.page_log2) * D;
   };
   auto scale_at = [&](int slot) { return (keys ? a.kscale : a.vscale) + (size_t)(slot >> a.page_log2) * a.H + h; };
+  static_assert(kAppendThreads >= kAppendSpan + 128, "the last run of a span ends within the tokens looked at");
   int slot, n;
   if (runs == 1) {
     const int t = run_of(0, &slot, &n);
