@@ -103,10 +103,29 @@ int hbl_kv_plan(const int32_t* new_lens, int B, int page, int num_pages, int max
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const kv::PlanArgs a{new_lens, kv_lens, block_table, free_pages, free_count, cu_q, slots, refused,
                        B, ilog2(page), num_pages, max_pages, T};
-  const size_t smem = 3 * ((size_t)B + 1) * 4;
+  const size_t smem = 4 * ((size_t)B + 1) * 4;
   ensure_smem_attr(kv::kv_plan_kernel, smem);
+  // a thread for each request or row up to a block's 1024; beyond that a cluster of blocks shares the rows
+  const int most = std::max(B, T), threads = most <= 128 ? 128 : most <= 512 ? 512 : kv::kPlanThreads;
+  const int ctas = T > 2 * kv::kPlanThreads ? kv::kPlanCtas : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   ProfScope ps("kv_plan", s);
-  kv::kv_plan_kernel<<<1, kv::kPlanThreads, smem, s>>>(a);
+  if (cudaLaunchKernelEx(&cfg, kv::kv_plan_kernel, a) != cudaSuccess) {
+    cudaGetLastError();
+    return HBL_ERR_CUDA;
+  }
   return launch_status();
 }
 

@@ -24,7 +24,8 @@ constexpr int kMaxRequests = 8192;
 // ---------------------------------------------------------------------------
 // Page planning.
 // ---------------------------------------------------------------------------
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;   // most threads of a block
+constexpr int kPlanCtas = 8;          // blocks of the cluster that takes a large step
 
 // Exclusive prefix sum over the block; *total gets the sum. `sh` holds 33 values.
 HBL_DEVINL long long block_scan(long long v, long long* sh, long long* total) {
@@ -78,27 +79,38 @@ struct PlanArgs {
 };
 
 // One step of the page table (see hbl_kv_plan). Every quantity is a prefix sum over the requests: rows of
-// new tokens, pages wanted, pages given back. With those three sums in shared memory, each slot, each
-// new table entry and each page returned to the stack is found by itself with a binary search.
+// new tokens, pages wanted, pages given back. With those sums in shared memory, each slot, each
+// new table entry and each page returned to the stack is found by itself with a binary search. A large step is taken by a
+// cluster of blocks: each forms the (short) sums for itself and takes its part of the rest; the lengths and the count,
+// which all of them read, are written behind a cluster barrier. Nothing here moves enough bytes to matter: it is bound
+// by its chain of dependent loads and barriers.
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(PlanArgs a) {
   extern __shared__ int sm[];
   int* cu = sm;                       // [B + 1] first row of each request
   int* want = cu + a.B + 1;           // [B + 1] pages taken by the requests before this one
   int* gone = want + a.B + 1;         // [B + 1] pages given back by the requests before this one
+  int* len = gone + a.B + 1;          // [B] cached tokens before the step; ~ of it where the request is refused
   __shared__ long long sh[33];
   __shared__ int s_used;
+  uint32_t rank, ranks;
+  asm("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(rank));
+  asm("mov.u32 %0, %%cluster_nctaid.x;\n" : "=r"(ranks));
+  const int tid = (int)(rank * blockDim.x + threadIdx.x), threads = (int)(ranks * blockDim.x);
   const int P = 1 << a.page_log2, lg = a.page_log2;
   const long long cap = (long long)a.max_pages << lg;
-  const int per = (a.B + kPlanThreads - 1) / kPlanThreads;
+  const int per = (a.B + (int)blockDim.x - 1) / (int)blockDim.x;
   const int b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
+  auto pages = [&](long long n) { return (int)((n + P - 1) >> lg); };
   if (threadIdx.x == 0) s_used = 0;
-
-  auto len_of = [&](int b) { return min(max((long long)a.kv_lens[b], 0ll), cap); };
-  auto pages = [&](long long n) { return (n + P - 1) >> lg; };
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const int F = min(max(*a.free_count, 0), a.num_pages);
 
   // rows of new tokens
   long long sum = 0, total;
-  for (int b = b0; b < b1; ++b) sum += max(a.new_lens[b], 0);
+  for (int b = b0; b < b1; ++b) {
+    len[b] = (int)min((long long)max(a.kv_lens[b], 0), cap);
+    sum += max(a.new_lens[b], 0);
+  }
   long long x = block_scan(sum, sh, &total);
   for (int b = b0; b < b1; ++b) {
     cu[b] = (int)min(x, (long long)a.T);
@@ -107,80 +119,75 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(PlanArgs a) {
   if (threadIdx.x == 0) cu[a.B] = (int)min(total, (long long)a.T);
   __syncthreads();
 
-  // pages wanted and given back; a request that cannot grow wants none
-  long long need = 0, back = 0;
+  // pages wanted (low word) and given back (high word); a request that cannot grow at all wants none
+  auto pages_of = [&](int b, bool* wide) {
+    const long long n = len[b], q = a.new_lens[b], after = max(n + q, 0ll);
+    *wide = q > 0 && (after > cap || cu[b + 1] - cu[b] < q);
+    if (*wide) return 0ll;
+    const int more = pages(after) - pages(n);
+    return more >= 0 ? (long long)more : (long long)(-more) << 32;
+  };
+  bool wide;
+  sum = 0;
+  for (int b = b0; b < b1; ++b) sum += pages_of(b, &wide);
+  x = block_scan(sum, sh, &total);
+  const int R = (int)(total >> 32), stock = (int)min((long long)F + R, 0x7fffffffll);
   for (int b = b0; b < b1; ++b) {
-    const long long n = len_of(b), q = a.new_lens[b], after = max(n + q, 0ll);
-    if (q > 0 && (after > cap || cu[b + 1] - cu[b] < q)) continue;
-    need += max(pages(after) - pages(n), 0ll);
-    back += max(pages(n) - pages(after), 0ll);
-  }
-  long long need_all, back_all;
-  const long long need0 = block_scan(need, sh, &need_all), back0 = block_scan(back, sh, &back_all);
-  const int F = min(max(*a.free_count, 0), a.num_pages);
-  const long long stock = F + back_all;
-  {
-    long long nd = need0, bk = back0;
-    for (int b = b0; b < b1; ++b) {
-      const long long n = len_of(b), q = a.new_lens[b], after = max(n + q, 0ll);
-      const bool wide = q > 0 && (after > cap || cu[b + 1] - cu[b] < q);
-      const long long take = wide ? 0 : max(pages(after) - pages(n), 0ll);
-      want[b] = (int)min(nd, 0x7fffffffll);
-      gone[b] = (int)min(bk, 0x7fffffffll);
-      const bool ok = !wide && (take == 0 || nd + take <= stock);
-      if (ok && take) atomicMax(&s_used, (int)(nd + take));
-      a.refused[b] = ok ? 0 : 1;
-      nd += take;
-      if (!wide) bk += max(pages(n) - pages(after), 0ll);
-    }
+    const long long y = pages_of(b, &wide);
+    const int take = (int)(y & 0xffffffff), nd = (int)(x & 0xffffffff);
+    want[b] = nd;
+    gone[b] = (int)(x >> 32);
+    const bool ok = !wide && (take == 0 || (long long)nd + take <= stock);
+    if (ok && take) atomicMax(&s_used, nd + take);
+    if (!ok) len[b] = ~len[b];
+    x += y;
   }
   if (threadIdx.x == 0) {
-    want[a.B] = (int)min(need_all, 0x7fffffffll);
-    gone[a.B] = (int)min(back_all, 0x7fffffffll);
+    want[a.B] = (int)(total & 0xffffffff);
+    gone[a.B] = R;
   }
   __syncthreads();
-  const int used = s_used, R = gone[a.B];
+  const int used = s_used;
 
   // i-th page given back in this step, and i-th page handed out: those given back first, then the stack from its top
   auto released = [&](int i) {
     const int b = find_row(gone, a.B, i);
-    const long long after = max(len_of(b) + a.new_lens[b], 0ll);
-    return a.table[(size_t)b * a.max_pages + (size_t)(pages(after) + (i - gone[b]))];
+    return a.table[(size_t)b * a.max_pages + (size_t)(pages(len[b]) - (gone[b + 1] - gone[b]) + (i - gone[b]))];
   };
   auto handed = [&](int i) { return i < R ? released(i) : a.free_pages[F - 1 - (i - R)]; };
 
-  for (int t = threadIdx.x; t < a.T; t += kPlanThreads) {
+  for (int t = tid; t < a.T; t += threads) {
     int slot = -1;
     if (t < cu[a.B]) {
-      const int b = find_row(cu, a.B, t);
-      if (a.refused[b] == 0) {
-        const long long n = len_of(b), pos = n + (t - cu[b]);
-        const int pi = (int)(pos >> lg), held = (int)pages(n);
+      const int b = find_row(cu, a.B, t), n = len[b];
+      if (n >= 0) {
+        const int pos = n + (t - cu[b]), pi = pos >> lg, held = pages(n);
         const int id = pi < held ? a.table[(size_t)b * a.max_pages + pi] : handed(want[b] + pi - held);
-        if (id >= 0 && id < a.num_pages) slot = (id << lg) + (int)(pos & (P - 1));
+        if (id >= 0 && id < a.num_pages) slot = (id << lg) + (pos & (P - 1));
         else set_device_error(HBL_ERR_INVALID_ARG);
       }
     }
     a.slots[t] = slot;
   }
-  for (int i = threadIdx.x; i < used; i += kPlanThreads) {
+  for (int i = tid; i < used; i += threads) {
     const int b = find_row(want, a.B, i);
-    a.table[(size_t)b * a.max_pages + (size_t)(pages(len_of(b)) + (i - want[b]))] = handed(i);
+    a.table[(size_t)b * a.max_pages + (size_t)(pages(len[b]) + (i - want[b]))] = handed(i);
   }
   // what was given back and not handed out again: the last of it lies deepest, so a step that is undone
   // leaves the stack as it was
-  for (int i = used + threadIdx.x; i < R; i += kPlanThreads) {
+  for (int i = used + tid; i < R; i += threads) {
     const int at = F + (R - 1 - i);
     if (at < a.num_pages) a.free_pages[at] = released(i);
     else set_device_error(HBL_ERR_INVALID_ARG);
   }
-  for (int b = threadIdx.x; b <= a.B; b += kPlanThreads) a.cu_q[b] = cu[b];
-  __syncthreads();
-  for (int b = b0; b < b1; ++b) {
-    const long long n = len_of(b);
-    a.kv_lens[b] = (int)(a.refused[b] ? n : max(n + a.new_lens[b], 0ll));
+  for (int b = tid; b <= a.B; b += threads) {
+    a.cu_q[b] = cu[b];
+    if (b < a.B) a.refused[b] = len[b] < 0;
   }
-  if (threadIdx.x == 0) *a.free_count = (int)min(stock - used, (long long)a.num_pages);
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+  for (int b = tid; b < a.B; b += threads)
+    a.kv_lens[b] = len[b] < 0 ? ~len[b] : (int)max((long long)len[b] + a.new_lens[b], 0ll);
+  if (tid == 0) *a.free_count = min(stock - used, a.num_pages);
 }
 
 // ---------------------------------------------------------------------------
