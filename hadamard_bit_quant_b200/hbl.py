@@ -74,11 +74,7 @@ def lib():
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    return x.data_ptr()
+    return x if x is None or isinstance(x, int) else x.data_ptr()
 
 
 def _stream(stream):

@@ -91,8 +91,10 @@ class KVStep(NamedTuple):
 
 
 def _index(*tensors):
+    """Index arrays: contiguous int32 on the current device, where the kernels are launched."""
+    dev = torch._C._cuda_getDevice()
     for x in tensors:
-        assert x.is_cuda and x.dtype == torch.int32 and x.is_contiguous()
+        assert x.get_device() == dev and x.dtype is torch.int32 and x.is_contiguous()
 
 
 class KVPages:
@@ -119,14 +121,14 @@ class KVPages:
 
     def plan(self, new_lens: torch.Tensor, tokens: int, out: KVStep | None = None, stream=None) -> KVStep:
         """Grow each request by new_lens[b] tokens (or drop -new_lens[b] of them): rows for ``tokens`` new ones."""
-        _index(new_lens)
+        _index(new_lens, self.kv_lens)
         B, max_pages = self.block_table.shape
-        assert new_lens.numel() == B and new_lens.device == self.kv_lens.device
+        assert new_lens.numel() == B
         if out is None:
-            new = new_lens.new_empty
-            out = KVStep(new(tokens), new(B + 1), new(B))
-        _index(*out)
-        assert out.slots.numel() == tokens and out.cu_q.numel() == B + 1 and out.refused.numel() == B
+            out = KVStep(*new_lens.new_empty(tokens + 2 * B + 1).split_with_sizes((tokens, B + 1, B)))
+        else:
+            _index(*out)
+            assert out.slots.numel() == tokens and out.cu_q.numel() == B + 1 and out.refused.numel() == B
         hbl.hbl_kv_plan(new_lens, B, self.page, self.free_pages.numel(), max_pages, tokens, self.kv_lens,
                         self.block_table, self.free_pages, self.free_count, out.cu_q, out.slots, out.refused, stream)
         return out
@@ -145,12 +147,13 @@ class KVCache:
     """
 
     def __init__(self, kcodes: torch.Tensor, vcodes: torch.Tensor, kscale: torch.Tensor, vscale: torch.Tensor):
-        assert kcodes.dim() == 4 and kcodes.shape == vcodes.shape and kscale.shape == vscale.shape == kcodes.shape[:2]
-        for c, s in ((kcodes, kscale), (vcodes, vscale)):
-            assert c.is_cuda and s.device == c.device and c.dtype == torch.uint8 and s.dtype == torch.float32
-            assert c.is_contiguous() and s.is_contiguous()
+        shape, dev = kcodes.shape, kcodes.get_device()
+        assert len(shape) == 4 and vcodes.shape == shape and kscale.shape == vscale.shape == shape[:2]
+        assert kcodes.dtype is vcodes.dtype is torch.uint8 and kscale.dtype is vscale.dtype is torch.float32
+        for x in (kcodes, vcodes, kscale, vscale):
+            assert x.is_contiguous() and x.get_device() == dev >= 0
         self.kcodes, self.vcodes, self.kscale, self.vscale = kcodes, vcodes, kscale, vscale
-        self.num_pages, self.kv_heads, self.page, self.head_dim = kcodes.shape
+        self.num_pages, self.kv_heads, self.page, self.head_dim = shape
 
     @classmethod
     def empty(cls, num_pages: int, kv_heads: int, page: int, head_dim: int, device="cuda") -> "KVCache":
@@ -161,15 +164,16 @@ class KVCache:
 
     def _rows(self, x: torch.Tensor, heads: int | None = None) -> int:
         """Elements from token to token of a [tokens, heads, head_dim] tensor whose tokens may lie apart."""
-        assert x.is_cuda and x.dtype == torch.bfloat16 and x.dim() == 3 and x.device == self.kcodes.device
+        assert x.dtype is torch.bfloat16 and x.get_device() == self.kcodes.get_device()
         T, H, D = x.shape
-        assert D == self.head_dim and H == (heads or H)
-        assert x.stride(2) == 1 and (H == 1 or x.stride(1) == D)
-        return x.stride(0) if T > 1 else H * D
+        st, sh, sd = x.stride()
+        assert D == self.head_dim and H == (heads or H) and sd == 1 and (H == 1 or sh == D)
+        return st if T > 1 else H * D
 
     def append(self, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
         """Quantise K and V (bf16 [T, kv_heads, head_dim], e.g. parts of one projection's output) into their slots."""
         _index(slots)
+        assert slots.get_device() == self.kcodes.get_device()
         ks, vs = self._rows(K, self.kv_heads), self._rows(V, self.kv_heads)
         T = K.shape[0]
         assert V.shape[0] == T and slots.numel() == T
@@ -179,6 +183,7 @@ class KVCache:
     def read(self, slots: torch.Tensor, stream=None):
         """The values in the given slots: (K, V), bf16 [T, kv_heads, head_dim]."""
         _index(slots)
+        assert slots.get_device() == self.kcodes.get_device()
         T = slots.numel()
         K, V = self.kcodes.new_empty((2, T, self.kv_heads, self.head_dim), dtype=torch.bfloat16)
         hbl.hbl_kv_read(slots, T, self.kv_heads, self.head_dim, self.page, self.num_pages, self.kcodes, self.vcodes,
@@ -201,18 +206,23 @@ class KVCache:
         _index(cu_q, kv_lens, block_table)
         stride = self._rows(Q)
         T, Hq, D = Q.shape
-        B = kv_lens.numel()
-        assert cu_q.numel() == B + 1 and block_table.dim() == 2 and block_table.shape[0] == B
+        B, max_pages = block_table.shape
+        assert kv_lens.numel() == B and cu_q.numel() == B + 1 and kv_lens.get_device() == self.kcodes.get_device()
         if out is None:
             out = Q.new_empty(T, Hq, D)
-        assert out.shape == Q.shape and out.dtype == torch.bfloat16 and out.is_contiguous() and out.device == Q.device
-        if lse is None and return_lse:
+        else:
+            assert out.shape == Q.shape and out.is_contiguous() and self._rows(out) == Hq * D
+        if lse is not None:
+            assert lse.shape == (T, Hq) and lse.dtype is torch.float32 and lse.is_contiguous()
+            assert lse.get_device() == Q.get_device()
+        elif return_lse:
             lse = self.kscale.new_empty(T, Hq)
-        assert lse is None or (lse.shape == (T, Hq) and lse.dtype == torch.float32 and lse.is_contiguous())
         if ws is None:
             ws = self.workspace(B)
+        else:
+            assert ws.dtype is torch.uint8 and ws.get_device() == Q.get_device()
         hbl.hbl_kv_attention(Q, T, Hq, self.kv_heads, D, stride, cu_q, kv_lens, B, max_q, max_kv, block_table,
-                             block_table.shape[1], self.page, self.num_pages, self.kcodes, self.vcodes, self.kscale,
-                             self.vscale, D ** -0.5 if scale is None else scale, int(causal), window, out, lse, ws,
+                             max_pages, self.page, self.num_pages, self.kcodes, self.vcodes, self.kscale, self.vscale,
+                             D ** -0.5 if scale is None else scale, int(causal), window, out, lse, ws,
                              ws.numel(), stream)
         return (out, lse) if return_lse else out
