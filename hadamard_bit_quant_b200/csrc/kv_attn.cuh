@@ -196,6 +196,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kAttnCtas) kv_attn_kernel(con
   __shared__ long long s_off;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t4 = lane & 3;
+  // the kernel that joins the parts may take its place as soon as there is room; it waits for this one's end
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
 
   Run run;

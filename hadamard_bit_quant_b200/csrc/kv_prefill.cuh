@@ -44,6 +44,7 @@ template <int D> struct __align__(1024) PreSmem {
   float scale[kPreRing][32];
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2], p_full[2][2], o_full[2];
   uint64_t drained[2];
+  float down[kPreRows];                  // a row's inverse power of two times the softmax scale
   long long sh[33];
   int item_b;
   int item_off;
@@ -193,6 +194,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
   S_t& S = *reinterpret_cast<S_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &S.abort;
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
 
   // the item of this CTA: request, head and row tile (longest first within a request)
@@ -285,36 +287,44 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     const int pos = rq.kv - rq.q + tok;
     const int last = a.causal ? max(min(rq.kv, pos + 1), 0) : rq.kv;
     const int first = a.window > 0 ? max(pos + 1 - a.window, 0) : 0;
-    float qs;
     {
-      // the row in fp16, brought into its range by a power of two, to shared memory
-      const uint4* src = reinterpret_cast<const uint4*>(a.Q + (size_t)(rq.row0 + tok) * (size_t)a.q_stride + (size_t)head * D);
-      float amax = 0.f;
-#pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 x = __ldg(src + c);
-        const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
+      // The warp's 32 rows in fp16, each brought into its range by a power of two, to shared memory: two (D = 64: four)
+      // rows at a time, a lane for each 16 bytes, so that the loads are whole lines.
+      constexpr int LPR = D / 8, RPI = 32 / LPR;           // lanes of a row, rows of a step
+      const int base = row0 + 128 * w + 32 * (warp & 3), c = lane % LPR;
+#pragma unroll 1
+      for (int i0 = 0; i0 < 32 / RPI; i0 += 8) {
+        uint4 x[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(ws[k] << 16)), fabsf(__uint_as_float(ws[k] & 0xffff0000u))));
-      }
-      float up;
-      row_power(amax, &up, &qs);
-      qs *= a.scale_log2;
-      const int rr = threadIdx.x & 127;
-#pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 x = __ldg(src + c);
-        const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
-        uint32_t o[4];
+        for (int i = 0; i < 8; ++i) {
+          const int rr = min(base + RPI * (i0 + i) + lane / LPR, nrows - 1);
+          x[i] = __ldg(reinterpret_cast<const uint4*>(a.Q + (size_t)(rq.row0 + rr / a.group) * (size_t)a.q_stride +
+                                                      (size_t)(h * a.group + rr % a.group) * D) + c);
+        }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          o[k] = pack_half(__uint_as_float(ws[k] << 16) * up, __uint_as_float(ws[k] & 0xffff0000u) * up);
-        sts128(tc::su32(&S.q[w][c >> 3][rr * 128 + (((c & 7) ^ (rr & 7)) << 4)]), make_uint4(o[0], o[1], o[2], o[3]));
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t ws[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          float amax = 0.f, up, down;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(ws[k] << 16)), fabsf(__uint_as_float(ws[k] & 0xffff0000u))));
+#pragma unroll
+          for (int d = 1; d < LPR; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+          row_power(amax, &up, &down);
+          const int rr = 32 * (warp & 3) + RPI * (i0 + i) + lane / LPR;
+          uint32_t o[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            o[k] = pack_half(__uint_as_float(ws[k] << 16) * up, __uint_as_float(ws[k] & 0xffff0000u) * up);
+          sts128(tc::su32(&S.q[w][c >> 3][rr * 128 + (((c & 7) ^ (rr & 7)) << 4)]), make_uint4(o[0], o[1], o[2], o[3]));
+          if (c == 0) S.down[128 * w + rr] = down * a.scale_log2;
+        }
       }
       fence_async_smem();
       tc::mbar_arrive(&S.q_full[w]);
+      __syncwarp();
     }
+    const float qs = S.down[threadIdx.x];
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t s_addr = lane_base + (uint32_t)(128 * w), o_addr = lane_base + (uint32_t)(256 + 128 * w);
     // keys that every row of this warp sees, for the tiles that need no mask
@@ -421,6 +431,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       const bool some = l > 0.f || l != l;
       const float inv = some ? vref / l : 0.f;
       const size_t out = (size_t)(rq.row0 + tok) * a.Hq + head;
+      // Each lane has a row; through the place of the half's queries, whose last use is over, a warp's stores become whole
+      // lines (two or four rows at a time).
+      constexpr int LPR = D / 8, RPI = 32 / LPR;
+      const int rr = threadIdx.x & 127;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t x[32];
@@ -428,20 +442,27 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
           HBL_TMEM_LD32(o_addr + 32u * c, x);
           tc::tc_wait_ld();
         }
-        if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(a.O + out * D + 32 * c);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t y[4];
+        for (int k = 0; k < 4; ++k) {
+          uint32_t y[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float e0 = some ? __uint_as_float(x[8 * k + 2 * i]) * inv : 0.f;
-              const float e1 = some ? __uint_as_float(x[8 * k + 2 * i + 1]) * inv : 0.f;
-              y[i] = (uint32_t)float_to_bf16_bits(e0) | ((uint32_t)float_to_bf16_bits(e1) << 16);
-            }
-            dst[k] = make_uint4(y[0], y[1], y[2], y[3]);
+          for (int i = 0; i < 4; ++i) {
+            const float e0 = some ? __uint_as_float(x[8 * k + 2 * i]) * inv : 0.f;
+            const float e1 = some ? __uint_as_float(x[8 * k + 2 * i + 1]) * inv : 0.f;
+            y[i] = (uint32_t)float_to_bf16_bits(e0) | ((uint32_t)float_to_bf16_bits(e1) << 16);
           }
+          const int ch = 4 * c + k;
+          sts128(tc::su32(&S.q[w][ch >> 3][rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)]), make_uint4(y[0], y[1], y[2], y[3]));
         }
+      }
+      __syncwarp();
+      const int base = row0 + 128 * w + 32 * (warp & 3), c = lane % LPR;
+#pragma unroll 4
+      for (int i = 0; i < 32 / RPI; ++i) {
+        const int r2 = 32 * (warp & 3) + RPI * i + lane / LPR, row = base + RPI * i + lane / LPR;
+        const uint4 v = lds128(tc::su32(&S.q[w][c >> 3][r2 * 128 + (((c & 7) ^ (r2 & 7)) << 4)]));
+        if (row < nrows)
+          reinterpret_cast<uint4*>(a.O + ((size_t)(rq.row0 + row / a.group) * a.Hq + (size_t)(h * a.group + row % a.group)) * D)[c] = v;
       }
       if (live && a.lse) a.lse[out] = some ? m * kLn2 + logf(l) : -INFINITY;
     }
