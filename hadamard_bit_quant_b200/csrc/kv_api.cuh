@@ -213,7 +213,9 @@ int hbl_kv_attention(const hbl_bf16* Q, int T, int Hq, int Hkv, int D, long long
                        reinterpret_cast<float*>(w + L.o), scale * kv::kLog2e, T, Hq, Hkv, Hq / Hkv, B, max_pages,
                        ilog2(page), num_pages, causal, window,
                        std::min(kv::kAttnCtas * d->sm_count, kv::kMaxAttnCtas), std::max(kFewRows, Hq / Hkv),
-                       (int)std::min<long long>((long long)(max_q ? max_q : T) * (Hq / Hkv), 0x7fffffffll), 0, 0};
+                       (int)std::min<long long>((long long)(max_q ? max_q : T) * (Hq / Hkv), 0x7fffffffll), 0, 0, 0, 0};
+  a.group_shift = ilog2(a.group);
+  a.group_mul = (uint32_t)((((1ull << a.group_shift) - (uint64_t)a.group) << 32) / (uint64_t)a.group + 1);
   a.tile_rows = std::min(a.most_rows, a.few_rows) <= 8 ? 8 : 16;
   // Few enough keys for one CTA to be through with them before a second kernel could have joined the parts: each item
   // is left whole (at most kWholeCtas of them, so that the grid stays a few waves).

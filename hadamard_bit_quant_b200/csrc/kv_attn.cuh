@@ -58,8 +58,15 @@ struct AttnArgs {
   int few_rows;                       // requests with more rows per key/value head than this go to kv_prefill_kernel
   int most_rows;                      // and those with more than this break the caller's bound
   int tile_rows;                      // query rows that kv_attn_kernel takes at a time: 8 or 16
+  uint32_t group_mul;                 // division by group: see by_group
+  int group_shift;
   int row_tiles;                      // > 0: one CTA for each request, head and of so many row tiles, nothing is split
 };
+
+// n / group for 0 <= n < 2^31 by one multiplication: with 2^shift >= group, group_mul = floor(2^32 (2^shift - group) / group) + 1.
+HBL_DEVINL int by_group(const AttnArgs& a, int n) {
+  return (int)((__umulhi((uint32_t)n, a.group_mul) + (uint32_t)n) >> a.group_shift);
+}
 
 // A request as the kernels see it: whatever the arrays hold, rows stay inside Q and keys inside the table.
 struct Request {
@@ -212,7 +219,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kAttnCtas) kv_attn_kernel(con
       const int row_lo = rt * 8 * NT, rows = min(8 * NT, run.rq.q * a.group - row_lo);
       for (int k = threadIdx.x; k < rows * (D / 8); k += blockDim.x) {
         const int r = row_lo + k / (D / 8);
-        const size_t out = (size_t)(run.rq.row0 + r / a.group) * a.Hq + (size_t)(h * a.group + r % a.group);
+        const int tok = by_group(a, r);
+        const size_t out = (size_t)(run.rq.row0 + tok) * a.Hq + (size_t)(h * a.group + r - tok * a.group);
         reinterpret_cast<uint4*>(a.O + out * D)[k % (D / 8)] = make_uint4(0, 0, 0, 0);
         if (a.lse && k % (D / 8) == 0) a.lse[out] = -INFINITY;
       }
@@ -348,7 +356,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kAttnCtas) kv_attn_kernel(con
     const Request& rq = run.rq;
     const int row_lo = run.rt * 8 * NT, rows = min(8 * NT, rq.q * a.group - row_lo);
     // keys that every row, and that any row, of the tile sees
-    const int tok_a = row_lo / a.group, tok_b = (row_lo + rows - 1) / a.group, pos0 = rq.kv - rq.q;
+    const int tok_a = by_group(a, row_lo), tok_b = by_group(a, row_lo + rows - 1), pos0 = rq.kv - rq.q;
     const int all_last = a.causal ? min(rq.kv, pos0 + tok_a + 1) : rq.kv;
     const int any_last = a.causal ? min(rq.kv, pos0 + tok_b + 1) : rq.kv;
     const int all_first = a.window > 0 ? max(pos0 + tok_b + 1 - a.window, 0) : 0;
@@ -360,8 +368,9 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kAttnCtas) kv_attn_kernel(con
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const int r = min(row_lo + 8 * i + g, rq.q * a.group - 1);
-      const uint16_t* q = a.Q + (size_t)(rq.row0 + r / a.group) * (size_t)a.q_stride +
-                          (size_t)(run.h * a.group + r % a.group) * D;
+      const int tok = by_group(a, r);
+      const uint16_t* q = a.Q + (size_t)(rq.row0 + tok) * (size_t)a.q_stride +
+                          (size_t)(run.h * a.group + r - tok * a.group) * D;
       uint32_t raw[NK][2];
       float amax = 0.f;
 #pragma unroll
@@ -451,7 +460,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kAttnCtas) kv_attn_kernel(con
           for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int pos = pos0 + min(row_lo + 8 * i + 2 * t4 + e, rq.q * a.group - 1) / a.group;
+              const int pos = pos0 + by_group(a, min(row_lo + 8 * i + 2 * t4 + e, rq.q * a.group - 1));
               const int last = a.causal ? min(rq.kv, pos + 1) : rq.kv;
               const int first = a.window > 0 ? pos + 1 - a.window : 0;
 #pragma unroll
@@ -607,7 +616,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kAttnCtas) kv_attn_kernel(con
           const int d = 4 * ch;
           if (final_) {
             const int row = row_lo + r;
-            const size_t out = (size_t)(rq.row0 + row / a.group) * a.Hq + (size_t)(run.h * a.group + row % a.group);
+            const int tok = by_group(a, row);
+            const size_t out = (size_t)(rq.row0 + tok) * a.Hq + (size_t)(run.h * a.group + row - tok * a.group);
             const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
             uint2 y;
             y.x = (uint32_t)float_to_bf16_bits(acc.x * inv) | ((uint32_t)float_to_bf16_bits(acc.y * inv) << 16);
@@ -651,7 +661,8 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const AttnArgs a, const
     const Request rq = request_of(a, b);
     if (r == 0 && h == 0 && k == 0 && lane == 0) check_bound(a, rq);
     mine = rq.few && r < rq.q * a.group;
-    row = (size_t)(rq.row0 + r / a.group) * a.Hq + (size_t)(h * a.group + r % a.group);
+    const int tok = by_group(a, r);
+    row = (size_t)(rq.row0 + tok) * a.Hq + (size_t)(h * a.group + r - tok * a.group);
     if (mine && rq.tiles > 0) {
       const long long total = a.prefix[a.B], n = min(total, (long long)a.ctas);
       const long long x0 = a.prefix[b] + (long long)(h * rq.rt + r / a.tile_rows) * rq.tiles, x1 = x0 + rq.tiles - 1;

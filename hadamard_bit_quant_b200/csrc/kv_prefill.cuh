@@ -167,8 +167,8 @@ struct TileRange { int lo, hi; };
 HBL_DEVINL TileRange tiles_seen(const AttnArgs& a, const Request& rq, int row_a, int row_b) {
   if (row_a > row_b) return {0, 0};
   const int pos0 = rq.kv - rq.q;
-  const int last = a.causal ? min(rq.kv, pos0 + row_b / a.group + 1) : rq.kv;
-  const int first = a.window > 0 ? max(pos0 + row_a / a.group + 1 - a.window, 0) : 0;
+  const int last = a.causal ? min(rq.kv, pos0 + by_group(a, row_b) + 1) : rq.kv;
+  const int first = a.window > 0 ? max(pos0 + by_group(a, row_a) + 1 - a.window, 0) : 0;
   if (last <= first) return {0, 0};
   return {first / kPreKeys, (last + kPreKeys - 1) / kPreKeys};
 }
@@ -195,6 +195,28 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &S.abort;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&S.q_full[i], 128);
+      tc::mbar_init(&S.k_full[i], 129);
+      tc::mbar_init(&S.k_empty[i], 2);
+      tc::mbar_init(&S.v_full[i], 128);
+      tc::mbar_init(&S.v_empty[i], 2);
+      tc::mbar_init(&S.s_full[i][0], 1);
+      tc::mbar_init(&S.s_full[i][1], 1);
+      tc::mbar_init(&S.p_full[i][0], 128);
+      tc::mbar_init(&S.p_full[i][1], 128);
+      tc::mbar_init(&S.o_full[i], 1);
+      tc::mbar_init(&S.drained[i], 1);
+    }
+    S.abort = 0;
+    S.item_b = -1;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == 12) {
+    tc::tmem_alloc(&S.tmem_base, 512);
+    tc::tmem_relinquish();
+  }
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
 
   // the item of this CTA: request, head and row tile (longest first within a request)
@@ -214,7 +236,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       if (lane >= o) ex += y;
     }
     if (lane == 31) S.sh[warp] = ex;
-    if (threadIdx.x == 0) S.item_b = -1;
     __syncthreads();
     for (int i = 0; i < warp; ++i) ex += S.sh[i];
     ex -= sum;
@@ -231,25 +252,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       }
     }
   }
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&S.q_full[i], 128);
-      tc::mbar_init(&S.k_full[i], 129);
-      tc::mbar_init(&S.k_empty[i], 2);
-      tc::mbar_init(&S.v_full[i], 128);
-      tc::mbar_init(&S.v_empty[i], 2);
-      tc::mbar_init(&S.s_full[i][0], 1);
-      tc::mbar_init(&S.s_full[i][1], 1);
-      tc::mbar_init(&S.p_full[i][0], 128);
-      tc::mbar_init(&S.p_full[i][1], 128);
-      tc::mbar_init(&S.o_full[i], 1);
-      tc::mbar_init(&S.drained[i], 1);
-    }
-    S.abort = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-  }
+  tc::tc_fence_before();
   __syncthreads();
-  if (S.item_b < 0) return;
+  tc::tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+  if (S.item_b < 0) {                    // more CTAs were launched than there are items
+    if (warp == 12) tc::tmem_dealloc(tmem, 512);
+    return;
+  }
   const int b = S.item_b;
   const Request rq = request_of(a, b);
   const int nrows = rq.q * a.group;
@@ -268,14 +278,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       lo = min(lo, half[w].lo);
       hi = max(hi, half[w].hi);
     }
-  if (warp == 12) {
-    tc::tmem_alloc(&S.tmem_base, 512);
-    tc::tmem_relinquish();
-  }
-  tc::tc_fence_before();
-  __syncthreads();
-  tc::tc_fence_after();
-  const uint32_t tmem = S.tmem_base;
 
   if (warp < 8) {
     // ----- a row's softmax -----
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     const int w = warp >> 2;
     const int r = row0 + 128 * w + (threadIdx.x & 127);
     const bool live = r < nrows;
-    const int tok = min(r, nrows - 1) / a.group, head = h * a.group + min(r, nrows - 1) % a.group;
+    const int tok = by_group(a, min(r, nrows - 1)), head = h * a.group + min(r, nrows - 1) - tok * a.group;
     const int pos = rq.kv - rq.q + tok;
     const int last = a.causal ? max(min(rq.kv, pos + 1), 0) : rq.kv;
     const int first = a.window > 0 ? max(pos + 1 - a.window, 0) : 0;
@@ -292,17 +294,16 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       // rows at a time, a lane for each 16 bytes, so that the loads are whole lines.
       constexpr int LPR = D / 8, RPI = 32 / LPR;           // lanes of a row, rows of a step
       const int base = row0 + 128 * w + 32 * (warp & 3), c = lane % LPR;
-#pragma unroll 1
-      for (int i0 = 0; i0 < 32 / RPI; i0 += 8) {
-        uint4 x[8];
+      uint4 x[32 / RPI];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int rr = min(base + RPI * (i0 + i) + lane / LPR, nrows - 1);
-          x[i] = __ldg(reinterpret_cast<const uint4*>(a.Q + (size_t)(rq.row0 + rr / a.group) * (size_t)a.q_stride +
-                                                      (size_t)(h * a.group + rr % a.group) * D) + c);
-        }
+      for (int i = 0; i < 32 / RPI; ++i) {
+        const int rr = min(base + RPI * i + lane / LPR, nrows - 1), t = by_group(a, rr);
+        x[i] = __ldg(reinterpret_cast<const uint4*>(a.Q + (size_t)(rq.row0 + t) * (size_t)a.q_stride +
+                                                    (size_t)(h * a.group + rr - t * a.group) * D) + c);
+      }
+      {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 32 / RPI; ++i) {
           const uint32_t ws[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
           float amax = 0.f, up, down;
 #pragma unroll
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
 #pragma unroll
           for (int d = 1; d < LPR; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
           row_power(amax, &up, &down);
-          const int rr = 32 * (warp & 3) + RPI * (i0 + i) + lane / LPR;
+          const int rr = 32 * (warp & 3) + RPI * i + lane / LPR;
           uint32_t o[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -461,8 +462,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       for (int i = 0; i < 32 / RPI; ++i) {
         const int r2 = 32 * (warp & 3) + RPI * i + lane / LPR, row = base + RPI * i + lane / LPR;
         const uint4 v = lds128(tc::su32(&S.q[w][c >> 3][r2 * 128 + (((c & 7) ^ (r2 & 7)) << 4)]));
+        const int t = by_group(a, row);
         if (row < nrows)
-          reinterpret_cast<uint4*>(a.O + ((size_t)(rq.row0 + row / a.group) * a.Hq + (size_t)(h * a.group + row % a.group)) * D)[c] = v;
+          reinterpret_cast<uint4*>(a.O + ((size_t)(rq.row0 + t) * a.Hq + (size_t)(h * a.group + row - t * a.group)) * D)[c] = v;
       }
       if (live && a.lse) a.lse[out] = some ? m * kLn2 + logf(l) : -INFINITY;
     }
@@ -611,7 +613,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       // Lane g < 8 holds those of group g. The key scale of a group that no row sees is 1, and none is below the
       // smallest that appending gives, so that a masked score (minus infinity) stays one when it is multiplied.
       const int32_t* table = a.table + (size_t)b * a.max_pages;
-      const int any_first = a.window > 0 ? max(rq.kv - rq.q + row0 / a.group + 1 - a.window, 0) : 0;
+      const int any_first = a.window > 0 ? max(rq.kv - rq.q + by_group(a, row0) + 1 - a.window, 0) : 0;
       float ks = 1.f, vs = 0.f, vref = 0.f;
       bool absent = false;
       PageLookup look;
