@@ -65,7 +65,7 @@ int launch_kv_attention(const kv::AttnArgs& a, cudaStream_t s) {
     auto kernel = a.tile_rows == 8 ? kv::kv_attn_kernel<D, 1> : kv::kv_attn_kernel<D, 2>;
     ensure_smem_attr(kernel, kv::AttnCfg<D>::kSmem);
     ProfScope ps("kv_attn", s);
-    launch_pdl(kernel, dim3(a.ctas), dim3(kv::kAttnWarps * 32), kv::AttnCfg<D>::kSmem, s, a);
+    launch_pdl(kernel, dim3(a.ctas), dim3(kv::AttnCfg<D>::kWarps * 32), kv::AttnCfg<D>::kSmem, s, a);
   }
   if (a.row_tiles == 0) {
     ProfScope ps("kv_combine", s);
@@ -212,7 +212,7 @@ int hbl_kv_attention(const hbl_bf16* Q, int T, int Hq, int Hkv, int D, long long
                        reinterpret_cast<long long*>(w + L.prefix), reinterpret_cast<float*>(w + L.ml),
                        reinterpret_cast<float*>(w + L.o), scale * kv::kLog2e, T, Hq, Hkv, Hq / Hkv, B, max_pages,
                        ilog2(page), num_pages, causal, window,
-                       std::min(kv::kAttnCtas * d->sm_count, kv::kMaxAttnCtas), std::max(kFewRows, Hq / Hkv),
+                       std::min((D == 64 ? kv::AttnCfg<64>::kCtas : kv::AttnCfg<128>::kCtas) * d->sm_count, kv::kMaxAttnCtas), std::max(kFewRows, Hq / Hkv),
                        (int)std::min<long long>((long long)(max_q ? max_q : T) * (Hq / Hkv), 0x7fffffffll), 0, 0, 0, 0};
   a.group_shift = ilog2(a.group);
   a.group_mul = (uint32_t)((((1ull << a.group_shift) - (uint64_t)a.group) << 32) / (uint64_t)a.group + 1);

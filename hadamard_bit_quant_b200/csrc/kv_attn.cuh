@@ -6,8 +6,8 @@
 //
 // The bound is the cache read: D bytes of keys and D of values for each token and head. The kernel is a stream over
 // tiles of 32 tokens:
-//   * two CTAs per SM, each with an equal share of all tiles of all requests and heads (the long axis is
-//     split wherever the share ends), tiles dealt to 6 warps in turn;
+//   * two or three CTAs per SM, each with an equal share of all tiles of all requests and heads (the long axis is
+//     split wherever the share ends), tiles dealt to its 6 or 4 warps in turn;
 //   * each warp has a ring of its own in shared memory, filled with 16-byte cp.async, and its own reference
 //     maximum, sum and output in registers: no barrier while it streams. The next run's first tiles are fetched before
 //     the warps' results of this one are added up;
@@ -28,13 +28,11 @@
 namespace hbl {
 namespace kv {
 
-constexpr int kAttnWarps = 6;
-constexpr int kAttnCtas = 2;          // blocks of an SM
 constexpr int kAttnTile = 32;         // tokens of a warp's tile
 constexpr int kAttnRows = 16;         // most query rows of a tile
 constexpr float kLag = 8.f;           // log2 of how far a tile may outgrow the reference maximum
 constexpr float kSlack = 16.f;        // and a value scale the reference scale
-constexpr int kMaxAttnCtas = 320;     // workspace is laid out for this many
+constexpr int kMaxAttnCtas = 480;     // workspace is laid out for this many
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -164,12 +162,16 @@ HBL_DEVINL void row_power(float amax, float* up, float* down) {
 // Shared memory of a CTA: each warp's ring of stages (32 tokens of keys, then of values, and 4 scales),
 // then the buffer through which the warps' outputs are added, four rows at a time.
 template <int D> struct AttnCfg {
+  // Warps of a block and blocks of an SM. Twelve warps hold enough bytes in flight; more and smaller blocks hide each
+  // other's beginnings and ends of runs, but leave more parts to be joined. Measured, 6 x 2 against 4 x 3: D = 64, 32
+  // requests of 5 rows, windows of 1024: 29.4 / 26.2 us; D = 128, one request of 131072: 56.9 / 58.7 us.
+  static constexpr int kWarps = D == 64 ? 4 : 6, kCtas = 12 / kWarps;
   static constexpr int kKBytes = kAttnTile * D;
   static constexpr int kStageBytes = 2 * kKBytes + 16;
   static constexpr int kStages = D == 128 ? 2 : 4;
-  static constexpr int kRing = kAttnWarps * kStages * kStageBytes;
-  static constexpr int kMerge = kAttnWarps * 4 * D * 4;
-  static constexpr int kSmem = kRing + kMerge + kAttnWarps * kAttnRows * 8;
+  static constexpr int kRing = kWarps * kStages * kStageBytes;
+  static constexpr int kMerge = kWarps * 4 * D * 4;
+  static constexpr int kSmem = kRing + kMerge + kWarps * kAttnRows * 8;
 };
 
 // 16-byte chunk c of token row r of a tile lies at chunk c ^ swz(r), chosen for the reads of a quarter-warp (two
@@ -193,8 +195,9 @@ struct Run {
 };
 
 template <int D, int NT>   // NT: column tiles of 8 query rows
-__global__ void __launch_bounds__(kAttnWarps * 32, kAttnCtas) kv_attn_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(AttnCfg<D>::kWarps * 32, AttnCfg<D>::kCtas) kv_attn_kernel(const AttnArgs a) {
   using C = AttnCfg<D>;
+  constexpr int kAttnWarps = C::kWarps;
   constexpr int NK = D / 16;          // k-steps of the score product
   constexpr int NJ = D / 16;          // row tiles of the output product
   extern __shared__ __align__(128) uint8_t smem[];

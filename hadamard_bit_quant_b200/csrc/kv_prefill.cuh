@@ -42,7 +42,7 @@ template <int D> struct __align__(1024) PreSmem {
   // of each tile: [0, 8) key scales of the 16-key groups, [8, 16) log2 of their value scales relative to the
   // reference, [16, 24) the inverses of those, [24] the reference, [25] bits of the groups that are not in the cache
   float scale[kPreRing][32];
-  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2], p_full[2][2], o_full[2];
+  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2], p_full[2][2], o_full[2], o_last[2];
   uint64_t drained[2];
   float down[kPreRows];                  // a row's inverse power of two times the softmax scale
   long long sh[33];
@@ -207,6 +207,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       tc::mbar_init(&S.p_full[i][0], 128);
       tc::mbar_init(&S.p_full[i][1], 128);
       tc::mbar_init(&S.o_full[i], 1);
+      tc::mbar_init(&S.o_last[i], 1);
       tc::mbar_init(&S.drained[i], 1);
     }
     S.abort = 0;
@@ -377,7 +378,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       l *= alpha;
       const float ao = alpha * shrink;
       if (n > 0 && __any_sync(0xffffffffu, ao != 1.f)) {
-        // Once the products so far are complete: the one before the last is, this step's scores came behind it.
+        // Once the products so far are complete. Those up to the last but one are (this step's scores were issued behind
+        // them), and the next one waits for this step, so the phase is either this one or just over.
         ok = __all_sync(0xffffffffu, wait(&S.o_full[w], (uint32_t)(n - 1) & 1u, abort));
         if (!ok) break;
         tc::tc_fence_after();
@@ -424,9 +426,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     }
     // ----- the row's output -----
     const bool any = steps > 0;
-    // all products but the last two are complete, so the two phases are told apart in turn
-    if (any) ok = ok && __all_sync(0xffffffffu, wait(&S.o_full[w], (uint32_t)steps & 1u, abort) &&
-                                                    wait(&S.o_full[w], (uint32_t)(steps - 1) & 1u, abort));
+    if (any) ok = ok && __all_sync(0xffffffffu, wait(&S.o_last[w], 0, abort));
     if (ok && !*abort) {
       tc::tc_fence_after();
       const bool some = l > 0.f || l != l;
@@ -594,6 +594,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         tc::tc_fence_after();
         outputs(t, part, n == 0);
         if (part) commit(&S.v_empty[t & 1]);
+        if (n == 2 * seen - 1) commit(&S.o_last[w]);
         if (t + 1 == t1) continue;
         if (part == 0) {
           if (!(ok = full(S.k_full, t + 1))) break;
