@@ -148,10 +148,15 @@ int hbl_kv_append(const hbl_bf16* K, const hbl_bf16* V, int T, int Hkv, int D, l
   // grid would else be smaller than two blocks for each place on the GPU.
   int span = std::max(page, 64);
   while (span > 8 && (long long)((T + span - 1) / span) * Hkv * 2 < 16ll * d->sm_count) span /= 2;
-  const dim3 grid((T + span - 1) / span, Hkv, 2);
+  const long long blocks = (long long)((T + span - 1) / span) * Hkv * 2;
+  if (blocks >= (1ll << 31)) return HBL_ERR_SHAPE;
+  const dim3 grid((unsigned)blocks);
   ProfScope ps("kv_append", s);
-  if (D == 64) launch_pdl(kv::kv_append_kernel<64>, grid, dim3(kv::kAppendThreads), 0, s, a, span);
-  else launch_pdl(kv::kv_append_kernel<128>, grid, dim3(kv::kAppendThreads), 0, s, a, span);
+  // what a run of a page holds for each thread: of a block, or of a warp where a page is a short run (16 tokens)
+  const bool many = page * D > 8192 || page * D == 16 * 128;
+  auto kernel = D == 64 ? (many ? kv::kv_append_kernel<64, 8> : kv::kv_append_kernel<64, 4>)
+                        : (many ? kv::kv_append_kernel<128, 8> : kv::kv_append_kernel<128, 4>);
+  launch_pdl(kernel, grid, dim3(kv::kAppendThreads), 0, s, a, span);
   return launch_status();
 }
 

@@ -260,11 +260,9 @@ struct AppendArgs {
 
 constexpr int kAppendThreads = 256;
 constexpr int kAppendSpan = 128;      // most tokens of a block's span; its last run may go on for a page
-constexpr int kAppendHeld = 8;        // 16-byte vectors that a thread holds
-
 // The tokens of one run, handled by `NT` threads (a warp or the block) of which this is number `tid`.
 // `reduce` gives all of them the largest of their values. What fits in registers is read once.
-template <int D, int NT, typename Reduce>
+template <int D, int NT, int HELD, typename Reduce>
 HBL_DEVINL void append_run(const uint16_t* x, long long stride, int n, int off, int P, uint8_t* codes, float* scale, int tid,
                            Reduce reduce) {
   constexpr int VPT = D / 8;          // vectors of a token
@@ -272,15 +270,17 @@ HBL_DEVINL void append_run(const uint16_t* x, long long stride, int n, int off, 
   const float held = off > 0 ? *scale : 0.f;
   const float before = held >= 0.f && held <= 3.4e38f ? held : 0.f;
   auto vec = [&](int i) { return __ldg(reinterpret_cast<const uint4*>(x + (size_t)(i / VPT) * (size_t)stride) + i % VPT); };
-  uint4 v[kAppendHeld];
+  uint4 v[HELD];
   uint32_t m = 0;
+  {
+    const uint16_t* p = x + (size_t)(tid / VPT) * (size_t)stride + 8 * (tid % VPT);
 #pragma unroll
-  for (int k = 0; k < kAppendHeld; ++k) {
-    v[k] = tid + k * NT < total ? vec(tid + k * NT) : make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < HELD; ++k, p += (NT / VPT) * stride)
+      v[k] = tid + k * NT < total ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
-  for (int k = 0; k < kAppendHeld; ++k) m = max_abs2(max_abs2(max_abs2(max_abs2(m, v[k].x), v[k].y), v[k].z), v[k].w);
-  for (int i = tid + kAppendHeld * NT; i < total; i += NT) {
+  for (int k = 0; k < HELD; ++k) m = max_abs2(max_abs2(max_abs2(max_abs2(m, v[k].x), v[k].y), v[k].z), v[k].w);
+  for (int i = tid + HELD * NT; i < total; i += NT) {
     const uint4 w = vec(i);
     m = max_abs2(max_abs2(max_abs2(max_abs2(m, w.x), w.y), w.z), w.w);
   }
@@ -294,7 +294,7 @@ HBL_DEVINL void append_run(const uint16_t* x, long long stride, int n, int off, 
     }
     top = reduce(max(m & 0xffffu, m >> 16));
 #pragma unroll
-    for (int k = 0; k < kAppendHeld; ++k)
+    for (int k = 0; k < HELD; ++k)
       v[k] = make_uint4(finite2(v[k].x), finite2(v[k].y), finite2(v[k].z), finite2(v[k].w));
   }
   const float s = fmaxf(before, fmaxf(__fdiv_rn(__uint_as_float(top << 16), 127.f), kScaleFloor));
@@ -312,9 +312,9 @@ HBL_DEVINL void append_run(const uint16_t* x, long long stride, int n, int off, 
   }
   uint2* dst = reinterpret_cast<uint2*>(codes + (size_t)off * D);
 #pragma unroll
-  for (int k = 0; k < kAppendHeld; ++k)
+  for (int k = 0; k < HELD; ++k)
     if (tid + k * NT < total) dst[tid + k * NT] = codes8(v[k], s, inv, h);
-  for (int i = tid + kAppendHeld * NT; i < total; i += NT) {
+  for (int i = tid + HELD * NT; i < total; i += NT) {
     uint4 w = vec(i);
     if (odd) w = make_uint4(finite2(w.x), finite2(w.y), finite2(w.z), finite2(w.w));
     dst[i] = codes8(w, s, inv, h);
@@ -326,16 +326,19 @@ HBL_DEVINL void append_run(const uint16_t* x, long long stride, int n, int off, 
 // tokens, for one head's keys or values: a single long one with all its threads, several (or a short one) with a
 // warp each. It finds the run's absmax, raises the block's scale to it if it must (rescaling the codes that the
 // block held before the run), and writes the run's codes; the values are read once, for both.
-template <int D>
+// HELD: 16-byte vectors that a thread holds, as many as a page gives it.
+template <int D, int HELD>
 __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const AppendArgs a, const int span) {
   constexpr int kWords = kAppendThreads / 32;
   __shared__ unsigned s_head[kWords], s_on[kWords];         // bit t: a run begins at token t0 + t; a run goes on there
   __shared__ int s_slot[kAppendThreads];
   __shared__ uint32_t s_max[2][kWords];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
-  const bool keys = blockIdx.z == 0;
-  const int P = 1 << a.page_log2, t0 = blockIdx.x * span;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // heads first, then keys and values: blocks that run together read whole token rows
+  const uint32_t unit = blockIdx.x / (uint32_t)a.H;
+  const int h = (int)(blockIdx.x - unit * (uint32_t)a.H), P = 1 << a.page_log2, t0 = (int)(unit >> 1) * span;
+  const bool keys = (unit & 1) == 0;
   const uint32_t slots = (uint32_t)a.num_pages << a.page_log2;
   {
     const int t = t0 + (int)threadIdx.x;
@@ -352,27 +355,30 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const Appe
     }
   }
   __syncthreads();
-  int runs = 0;
+  const unsigned heads = lane < kWords ? s_head[lane] : 0u, on = lane < kWords ? s_on[lane] : 0u;
+  int upto = __popc(heads);           // runs that begin in this lane's word or before it
 #pragma unroll
-  for (int i = 0; i < kWords; ++i) runs += __popc(s_head[i]);
+  for (int d = 1; d < kWords; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += y;
+  }
+  const int runs = __shfl_sync(0xffffffffu, upto, kWords - 1);
   if (runs == 0) return;
   const uint16_t* x = keys ? a.k : a.v;
   const long long stride = keys ? a.kstride : a.vstride;
-  // token, slot and length of the i-th run
-  auto run_of = [&](int i, int* slot, int* n) {
-    int w = 0;
-    while (i >= __popc(s_head[w])) i -= __popc(s_head[w++]);
-    unsigned b = s_head[w];
-    for (; i > 0; --i) b &= b - 1;
-    const int t = 32 * w + __ffs(b) - 1;
+  // Token, slot and length of the i-th run, by a whole warp: lane l looks at the tokens 32 l to 32 l + 31.
+  auto run_at = [&](int i, int* slot, int* n) {
+    const int word = __ffs(__ballot_sync(0xffffffffu, lane < kWords && upto > i)) - 1;
+    unsigned bits = __shfl_sync(0xffffffffu, heads, word);
+    for (int skip = i - (__shfl_sync(0xffffffffu, upto, word) - __popc(bits)); skip > 0; --skip) bits &= bits - 1;
+    const int t = 32 * word + __ffs(bits) - 1;
+    // the first token behind t where no run goes on
+    unsigned stop = lane < kWords ? ~on : 0u;
+    if (lane < word) stop = 0;
+    else if (lane == word) stop &= ~(0xffffffffu >> (31 - (t & 31)));
+    const int end = __reduce_min_sync(0xffffffffu, stop ? 32 * lane + __ffs(stop) - 1 : kAppendThreads);
     *slot = s_slot[t];
-    int end = t + 1;
-    while (end < kAppendThreads) {
-      const unsigned stop = ~s_on[end >> 5] >> (end & 31);
-      if (stop) { end += __ffs(stop) - 1; break; }
-      end = (end | 31) + 1;
-    }
-    *n = min(end, kAppendThreads) - t;
+    *n = end - t;
     return t0 + t;
   };
   auto codes_at = [&](int slot) {
@@ -382,26 +388,25 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const Appe
   static_assert(kAppendThreads >= kAppendSpan + 128, "the last run of a span ends within the tokens looked at");
   int slot, n;
   if (runs == 1) {
-    const int t = run_of(0, &slot, &n);
+    const int t = run_at(0, &slot, &n);
     if (n * (D / 8) > 4 * 32) {
       int pass = 0;
-      append_run<D, kAppendThreads>(x + (size_t)t * (size_t)stride + (size_t)h * D, stride, n, slot & (P - 1), P, codes_at(slot),
-                                    scale_at(slot), threadIdx.x, [&](uint32_t m) {
+      append_run<D, kAppendThreads, HELD>(x + (size_t)t * (size_t)stride + (size_t)h * D, stride, n, slot & (P - 1), P,
+                                          codes_at(slot), scale_at(slot), threadIdx.x, [&](uint32_t m) {
         m = __reduce_max_sync(0xffffffffu, m);
         if (lane == 0) s_max[pass][warp] = m;
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kAppendThreads / 32; ++i) m = max(m, s_max[pass][i]);
+        m = __reduce_max_sync(0xffffffffu, lane < kWords ? s_max[pass][lane] : 0u);
         pass ^= 1;
         return m;
       });
       return;
     }
   }
-  for (int i = warp; i < runs; i += kAppendThreads / 32) {
-    const int t = run_of(i, &slot, &n);
-    append_run<D, 32>(x + (size_t)t * (size_t)stride + (size_t)h * D, stride, n, slot & (P - 1), P, codes_at(slot), scale_at(slot),
-                      lane, [&](uint32_t m) { return __reduce_max_sync(0xffffffffu, m); });
+  for (int i = warp; i < runs; i += kWords) {
+    const int t = run_at(i, &slot, &n);
+    append_run<D, 32, HELD>(x + (size_t)t * (size_t)stride + (size_t)h * D, stride, n, slot & (P - 1), P, codes_at(slot),
+                            scale_at(slot), lane, [&](uint32_t m) { return __reduce_max_sync(0xffffffffu, m); });
   }
 }
 
