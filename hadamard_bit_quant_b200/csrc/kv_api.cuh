@@ -72,7 +72,8 @@ int launch_kv_attention(const kv::AttnArgs& a, cudaStream_t s) {
     // few rows have many parts, many rows have few
     const int rows = std::min(a.few_rows, a.most_rows);
     const long long all = (long long)a.B * a.Hkv * rows;
-    if (all <= 1024) launch_pdl(kv::kv_combine_kernel<D, 4>, dim3((unsigned)((all + 1) / 2)), dim3(256), 0, s, a, rows);
+    if (all <= 256) launch_pdl(kv::kv_combine_kernel<D, 8>, dim3((unsigned)all), dim3(256), 0, s, a, rows);
+    else if (all <= 1024) launch_pdl(kv::kv_combine_kernel<D, 2>, dim3((unsigned)((all + 3) / 4)), dim3(256), 0, s, a, rows);
     else launch_pdl(kv::kv_combine_kernel<D, 1>, dim3((unsigned)((all + 7) / 8)), dim3(256), 0, s, a, rows);
   }
   return launch_status();

@@ -352,7 +352,29 @@ __global__ void __launch_bounds__(AttnCfg<D>::kWarps * 32, AttnCfg<D>::kCtas) kv
     }
   };
 
+  // A run's query rows (row g of each column tile), asked for ahead of its first tiles: behind them they would wait for
+  // everything that the whole GPU has just asked for.
+  uint32_t raw[NT][NK][2];
+  auto queries = [&](const Run& r) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int row = min(r.rt * 8 * NT + 8 * i + g, r.rq.q * a.group - 1), tok = by_group(a, row);
+      const uint16_t* q = a.Q + (size_t)(r.rq.row0 + tok) * (size_t)a.q_stride + (size_t)(r.h * a.group + row - tok * a.group) * D;
+#pragma unroll
+      for (int c = 0; c < NK / 4; ++c) {
+        const uint4* p = reinterpret_cast<const uint4*>(q + 16 * (t4 + 4 * c));
+        const uint4 x = __ldg(p), y = __ldg(p + 1);
+        const uint32_t ws[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          raw[i][4 * c + k][0] = ws[2 * k];
+          raw[i][4 * c + k][1] = ws[2 * k + 1];
+        }
+      }
+    }
+  };
   open(run);
+  queries(run);
   fill(run);
   bool first_item = true;
   while (true) {
@@ -370,29 +392,13 @@ __global__ void __launch_bounds__(AttnCfg<D>::kWarps * 32, AttnCfg<D>::kCtas) kv
     float qs[NT][2];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const int r = min(row_lo + 8 * i + g, rq.q * a.group - 1);
-      const int tok = by_group(a, r);
-      const uint16_t* q = a.Q + (size_t)(rq.row0 + tok) * (size_t)a.q_stride +
-                          (size_t)(run.h * a.group + r - tok * a.group) * D;
-      uint32_t raw[NK][2];
       float amax = 0.f;
-#pragma unroll
-      for (int c = 0; c < NK / 4; ++c) {
-        const uint4* p = reinterpret_cast<const uint4*>(q + 16 * (t4 + 4 * c));
-        const uint4 x = __ldg(p), y = __ldg(p + 1);
-        const uint32_t ws[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          raw[4 * c + k][0] = ws[2 * k];
-          raw[4 * c + k][1] = ws[2 * k + 1];
-        }
-      }
 #pragma unroll
       for (int k = 0; k < NK; ++k)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(raw[k][e] << 16)),
-                                   fabsf(__uint_as_float(raw[k][e] & 0xffff0000u))));
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(raw[i][k][e] << 16)),
+                                   fabsf(__uint_as_float(raw[i][k][e] & 0xffff0000u))));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       float up, down;
@@ -404,7 +410,7 @@ __global__ void __launch_bounds__(AttnCfg<D>::kWarps * 32, AttnCfg<D>::kCtas) kv
       for (int k = 0; k < NK; ++k)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          qf[i][k][e] = pack_half(__uint_as_float(raw[k][e] << 16) * up, __uint_as_float(raw[k][e] & 0xffff0000u) * up);
+          qf[i][k][e] = pack_half(__uint_as_float(raw[i][k][e] << 16) * up, __uint_as_float(raw[i][k][e] & 0xffff0000u) * up);
     }
 
     // this thread's rows are 8 i + 2 t4 + e; output tile jj holds the channels 2 NJ g + 2 jj and the next one
@@ -568,6 +574,7 @@ __global__ void __launch_bounds__(AttnCfg<D>::kWarps * 32, AttnCfg<D>::kCtas) kv
     __syncwarp();
     if (more) {
       open(next);
+      queries(next);
       fill(next);
     }
 
@@ -676,18 +683,36 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const AttnArgs a, const
       if (mine) {
         // the first part is its CTA's last item, unless the CTA begins with it; every other one is its CTA's first
         const int tail = total * c0 / n != x0;
-        for (int c = c0 + k; c <= c1; c += KW) {
-          const size_t slot = ((size_t)c * 2 + (c == c0 ? tail : 0)) * kAttnRows + r % a.tile_rows;
-          const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * slot);
-          float v[V];
-          if constexpr (V == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(a.part_o + slot * D + V * lane);
-          else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(a.part_o + slot * D + V * lane);
-          const float mn = fmaxf(M, ml.x), mu = mn == -INFINITY ? 0.f : mn;
-          const float f0 = exp2_fast(M - mu), f1 = exp2_fast(ml.x - mu);
-          M = mn;
-          L = L * f0 + ml.y * f1;
+        for (int c = c0 + k; c <= c1; c += 4 * KW) {        // four parts at a time, all asked for before the first is used
+          float2 ml[4];
+          float v[4][V];
 #pragma unroll
-          for (int e = 0; e < V; ++e) acc[e] = acc[e] * f0 + v[e] * f1;
+          for (int p = 0; p < 4; ++p) {
+            const int at = c + p * KW;
+            ml[p] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[p][e] = 0.f;
+            if (at <= c1) {
+              const size_t slot = ((size_t)at * 2 + (at == c0 ? tail : 0)) * kAttnRows + r % a.tile_rows;
+              ml[p] = *reinterpret_cast<const float2*>(a.part_ml + 2 * slot);
+              const float* o = a.part_o + slot * D + V * lane;
+              if constexpr (V == 4) *reinterpret_cast<float4*>(v[p]) = *reinterpret_cast<const float4*>(o);
+              else *reinterpret_cast<float2*>(v[p]) = *reinterpret_cast<const float2*>(o);
+            }
+          }
+          const float mn = fmaxf(M, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
+          const float mu = mn == -INFINITY ? 0.f : mn, f0 = exp2_fast(M - mu);
+          M = mn;
+          L *= f0;
+#pragma unroll
+          for (int e = 0; e < V; ++e) acc[e] *= f0;
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const float f = exp2_fast(ml[p].x - mu);
+            L += ml[p].y * f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] += v[p][e] * f;
+          }
         }
       }
     }
