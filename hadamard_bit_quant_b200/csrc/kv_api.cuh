@@ -25,6 +25,11 @@ int check_heads(int T, int H, int D) {
   return HBL_OK;
 }
 
+int check_table(int B, int max_pages, int page) {
+  if (B < 0 || B > kv::kMaxRequests || max_pages < 1 || (long long)B * max_pages >= (1ll << 31)) return HBL_ERR_SHAPE;
+  return (long long)max_pages * page > (1ll << 30) ? HBL_ERR_SHAPE : HBL_OK;
+}
+
 struct KvWs {
   size_t prefix, ml, o, total;
 };
@@ -89,9 +94,7 @@ int hbl_kv_plan(const int32_t* new_lens, int B, int page, int num_pages, int max
                 int32_t* refused, hbl_stream stream) {
   int st = check_pages(page, num_pages);
   if (st) return st;
-  if (B < 0 || B > kv::kMaxRequests || T < 0 || max_pages < 1 || (long long)B * max_pages >= (1ll << 31) ||
-      (long long)max_pages * page >= (1ll << 31))
-    return HBL_ERR_SHAPE;
+  if (T < 0 || (st = check_table(B, max_pages, page))) return HBL_ERR_SHAPE;
   if (B == 0) return HBL_OK;
   if (!new_lens || !kv_lens || !block_table || !free_pages || !free_count || !cu_q || !refused || (T > 0 && !slots))
     return HBL_ERR_INVALID_ARG;
@@ -195,9 +198,8 @@ int hbl_kv_attention(const hbl_bf16* Q, int T, int Hq, int Hkv, int D, long long
   int st = check_pages(page, num_pages);
   if (st || (st = check_heads(T, Hq, D)) || (st = check_heads(T, Hkv, D))) return st;
   if (Hq % Hkv != 0 || q_stride < (long long)Hq * D || q_stride % 8) return HBL_ERR_SHAPE;
-  if (B < 0 || B > kv::kMaxRequests || max_pages < 1 || (long long)B * max_pages >= (1ll << 31) ||
-      (long long)max_pages * page >= (1ll << 31))
-    return HBL_ERR_SHAPE;
+  // positions, rows and windows (cut to the table's reach below) then add up within an int
+  if ((long long)T * Hq >= (1ll << 30) || (st = check_table(B, max_pages, page))) return HBL_ERR_SHAPE;
   if (max_q < 0 || max_kv < 0) return HBL_ERR_SHAPE;
   if ((causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal)) return HBL_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale)) return HBL_ERR_INVALID_ARG;
@@ -217,7 +219,7 @@ int hbl_kv_attention(const hbl_bf16* Q, int T, int Hq, int Hkv, int D, long long
   kv::AttnArgs a{Q, q_stride, cu_q, kv_lens, block_table, kcodes, vcodes, kscale, vscale, O, lse,
                        reinterpret_cast<long long*>(w + L.prefix), reinterpret_cast<float*>(w + L.ml),
                        reinterpret_cast<float*>(w + L.o), scale * kv::kLog2e, T, Hq, Hkv, Hq / Hkv, B, max_pages,
-                       ilog2(page), num_pages, causal, window,
+                       ilog2(page), num_pages, causal, window < max_pages * page ? window : 0,
                        std::min((D == 64 ? kv::AttnCfg<64>::kCtas : kv::AttnCfg<128>::kCtas) * d->sm_count, kv::kMaxAttnCtas), std::max(kFewRows, Hq / Hkv),
                        (int)std::min<long long>((long long)(max_q ? max_q : T) * (Hq / Hkv), 0x7fffffffll), 0, 0, 0, 0};
   a.group_shift = ilog2(a.group);

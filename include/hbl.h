@@ -272,7 +272,8 @@ int hbl_quantize_qkv(const hbl_bf16* X, int T, int H, int d, int bits, int bos_t
  *   kscale, vscale : device fp32, num_pages x Hkv.
  * D is 64 or 128. A slot is a place for one token: page index * page + offset;
  * num_pages * page < 2^31. Request b of a batch has kv_lens[b] tokens, token j
- * in page block_table[b][j / page] (device int32, B x max_pages). All index
+ * in page block_table[b][j / page] (device int32, B x max_pages, B <= 8192,
+ * B * max_pages < 2^31, max_pages * page <= 2^30). All index
  * arrays are device int32, their contents are read by the kernels only, and
  * may change between replays of a captured call.
  * Index arrays and scales need 4-byte alignment, everything else 16-byte.
@@ -306,7 +307,7 @@ int hbl_quantize_qkv(const hbl_bf16* X, int T, int H, int d, int bits, int bos_t
  *                pages ran out, then also for every later request that needs
  *                a page). A refused request keeps its length and pages; its
  *                rows in cu_q are of no use to attention.
- * B <= 8192. Requests of one batch share no page that this step writes.
+ * Requests of one batch share no page that this step writes.
  */
 int hbl_kv_plan(const int32_t* new_lens, int B, int page, int num_pages, int max_pages, int T,
                 int32_t* kv_lens, int32_t* block_table, int32_t* free_pages, int32_t* free_count,
@@ -367,7 +368,10 @@ size_t hbl_kv_attention_workspace_bytes(int B, int D);
  *             execution overlaps must not share it.
  * A row that sees no key gives zeros and an lse of -infinity. A key whose
  * page is not in the cache counts as absent. Masked keys have no influence,
- * whatever they hold. Scales must be finite. B <= 8192, T * Hq < 2^31.
+ * whatever they hold. Scales must be finite and not negative. Scores, sums and
+ * outputs are fp32; probabilities are rounded to fp16 relative to the largest
+ * of a row's value scales (an absolute error of at most 2^-25 for each key where they
+ * are small). T * Hq < 2^30.
  */
 int hbl_kv_attention(const hbl_bf16* Q, int T, int Hq, int Hkv, int D, long long q_stride,
                      const int32_t* cu_q, const int32_t* kv_lens, int B, int max_q, int max_kv,

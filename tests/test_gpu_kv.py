@@ -71,6 +71,28 @@ def test_plan(L, B, page, max_pages, spare, most, T, seed):
         free = pages.free_pages.cpu().numpy()
 
 
+def test_plan_survives_any_state(L):
+    """Lengths, counts and page numbers that no step could have left: nothing out of bounds, what is bad is recorded."""
+    from hadamard_bit_quant_b200 import hbl
+    rng = np.random.default_rng(5)
+    B, width, num = 50, 4, 30
+    huge = rng.integers(-2 ** 31, 2 ** 31, 5 * B)
+    guard = torch.full((num + 64,), 77, dtype=torch.int32, device="cuda")       # what lies behind the stack stays
+    guard[:num] = i32(rng.integers(-2 ** 31, 2 ** 31, num))
+    for new in (huge[:B], np.full(B, 3), np.full(B, -2 ** 31), rng.integers(-70, 70, B)):
+        table = i32(rng.integers(-2 ** 31, 2 ** 31, (B, width)))
+        pages = L.KVPages(i32(huge[B:2 * B]), table, guard[:num], i32([2 ** 31 - 1]), 16)
+        step = pages.plan(i32(new), 200)
+        slots = step.slots.cpu().numpy()
+        assert np.all((slots >= -1) & (slots < num * 16))
+        assert 0 <= int(pages.free_count) <= num and bool((guard[num:] == 77).all())
+        lens = pages.kv_lens.cpu().numpy()
+        assert np.all((lens >= 0) & (lens <= width * 16))
+        cu = step.cu_q.cpu().numpy()
+        assert cu[0] == 0 and np.all(np.diff(cu) >= 0) and cu[-1] <= 200
+    assert hbl.hbl_get_device_error() == 1
+
+
 def test_plan_dropping_a_step_restores_the_stack(L):
     rng = np.random.default_rng(3)
     kv, table, free, count, num = random_state(rng, 20, 16, 10, 40)
@@ -290,7 +312,7 @@ def test_attention_long_prompts(L, Hq, Hkv, D, page, causal, window):
 
 def test_attention_prompts_of_all_scales(L):
     """Zero scales, and first tiles that a row does not see at all."""
-    case = make_case(L, 16, [300, 100], [300, 60], 2, 1, 128, 32)
+    case = make_case(L, 16, [300, 100, 90], [300, 60, 0], 2, 1, 128, 32)      # the last has no key at all
     check(L, case)
     case[0].vscale[:] = 0
     check(L, case)
@@ -308,6 +330,50 @@ def test_attention_rows_beyond_the_bound_are_left(L):
     assert hbl.hbl_get_device_error() == 1
     assert bool((out[2:] == 7).all())
     assert torch.equal(out[:2], cache.attention(Q, i32(cu), i32(kvs), i32(table))[:2])
+
+
+def test_attention_widest_window_and_rows(L):
+    """A window as wide as an int and more rows than keys: no limit of the kernels' own shows."""
+    case = make_case(L, 18, [5, 300], [2, 100], 2, 1, 64, 16)
+    cache, Q, cu, kvs, table = case
+    want = check(L, case)
+    got = cache.attention(Q, i32(cu), i32(kvs), i32(table), window=2 ** 31 - 1, return_lse=True)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+@pytest.mark.parametrize("kvs", [[130], [512, 1, 0], [513, 40, 33]])
+def test_attention_short_and_split_agree(L, kvs):
+    """The same rows by one block each (short contexts) and split between blocks."""
+    case = make_case(L, 19, [1] * len(kvs), kvs, 8, 4, 128, 32, width=20)
+    cache, Q, cu, kv, table = case
+    want = reference(*case)
+    for kw in ({"max_q": 1, "max_kv": max(kvs)}, {"max_q": 1}, {"max_q": 1, "max_kv": 5}):
+        out, lse = cache.attention(Q, i32(cu), i32(kv), i32(table), return_lse=True, **kw)
+        close(out, lse, want, float(cache.vscale.max()), max(kvs))
+
+
+def test_layer_refuses(L):
+    case = make_case(L, 20, [1, 1], [40, 30], 4, 2, 64, 16)
+    cache, Q, cu, kvs, table = case
+    cu, kvs, table = i32(cu), i32(kvs), i32(table)
+    for bad in (lambda: cache.attention(Q.float(), cu, kvs, table), lambda: cache.attention(Q, cu.long(), kvs, table),
+                lambda: cache.attention(Q, cu[:-1], kvs, table), lambda: cache.attention(Q.cpu(), cu, kvs, table),
+                lambda: cache.attention(Q, cu.cpu(), kvs, table), lambda: cache.attention(Q[..., :32], cu, kvs, table),
+                lambda: cache.attention(Q, cu, kvs, table[:1]), lambda: cache.attention(Q, cu, kvs, table, out=Q.float()),
+                lambda: cache.append(Q, Q, kvs), lambda: cache.append(Q[:, :2], Q[:1, :2], kvs),
+                lambda: cache.read(kvs.float()), lambda: L.KVCache(cache.kcodes, cache.vcodes[:1], cache.kscale, cache.vscale),
+                lambda: L.KVCache(cache.kcodes.cpu(), cache.vcodes, cache.kscale, cache.vscale),
+                lambda: L.KVPages(kvs, table.t(), kvs, kvs[:1], 16)):
+        with pytest.raises((AssertionError, ValueError)):
+            bad()
+    from hadamard_bit_quant_b200.hbl import HblError
+    for bad in (lambda: cache.attention(Q, cu, kvs, table, window=-1), lambda: cache.attention(Q, cu, kvs, table, scale=0.0),
+                lambda: cache.attention(Q, cu, kvs, table, causal=False, window=3),
+                lambda: cache.attention(Q[:, :3].contiguous(), cu, kvs, table),
+                lambda: cache.attention(Q, cu, kvs, table, ws=torch.empty(256, dtype=torch.uint8, device="cuda")),
+                lambda: L.KVPages(kvs, table, kvs, kvs[:1], 20).plan(kvs, 4)):
+        with pytest.raises(HblError):
+            bad()
 
 
 def test_attention_hints_do_not_change_results(L):
@@ -342,6 +408,30 @@ def test_attention_scales_of_all_sizes(L):
     Q.copy_((Q.float() * 1e30).to(torch.bfloat16))
     Q.mul_(1e30)
     check(L, case)
+
+
+def test_cache_beyond_32_bit_offsets(L):
+    """Pages more than 4 GiB into the cache: the same bits as in a small cache."""
+    H, D, page, T = 8, 128, 64, 300
+    far = L.KVCache(*(torch.empty(66000, H, page, D, dtype=torch.uint8, device="cuda") for _ in range(2)),
+                    *(torch.zeros(66000, H, device="cuda") for _ in range(2)))
+    near = L.KVCache.empty(8, H, page, D)
+    ids = [65999, 3, 65700, 65536, 65998]
+    pos = np.arange(T)
+    slots = [i32(np.array(p)[pos // page] * page + pos % page) for p in (ids, [0, 1, 2, 3, 4])]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(T, 2 * H, D, generator=g, device="cuda").to(torch.bfloat16)
+    Q = torch.randn(T, 2 * H, D, generator=g, device="cuda").to(torch.bfloat16)
+    outs = []
+    for cache, s, p in ((far, slots[0], ids), (near, slots[1], [0, 1, 2, 3, 4])):
+        cache.append(x[:250, :H], x[:250, H:], s[:250])
+        cache.append(x[250:, :H], x[250:, H:], s[250:])       # rescales what the page holds
+        table = i32([p])
+        outs.append((*cache.read(s), *cache.attention(Q, i32([0, T]), i32([T]), table, return_lse=True),
+                     cache.attention(Q[:1], i32([0, 1]), i32([T]), table)))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    assert torch.equal(far.kcodes[65999], near.kcodes[0]) and torch.equal(far.vscale[ids], near.vscale[:5])
 
 
 def test_attention_what_is_masked_has_no_influence(L):

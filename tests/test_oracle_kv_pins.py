@@ -144,7 +144,7 @@ def attention_args(**kw):
 @pytest.mark.parametrize("kw,status", [
     ({"page": 8}, 2), ({"page": 48}, 2), ({"page": 256}, 2), ({"num_pages": 0}, 2), ({"num_pages": 1 << 27}, 2),
     ({"B": -1}, 2), ({"B": 8193}, 2), ({"T": -1}, 2), ({"max_pages": 0}, 2), ({"max_pages": 1 << 30}, 2),
-    ({"new_lens": None}, 1), ({"kv_lens": None}, 1), ({"block_table": None}, 1), ({"free_pages": None}, 1),
+    ({"max_pages": (1 << 26) + 1}, 2), ({"B": 8192, "max_pages": 1 << 18}, 2), ({"new_lens": None}, 1), ({"kv_lens": None}, 1), ({"block_table": None}, 1), ({"free_pages": None}, 1),
     ({"free_count": None}, 1), ({"cu_q": None}, 1), ({"slots": None}, 1), ({"refused": None}, 1), ({"slots": A + 2}, 1),
     ({"B": 0, "kv_lens": None}, 0)])
 def test_plan_refusals(lib, kw, status):
@@ -170,7 +170,7 @@ def test_read_refusals(lib, kw, status):
 
 @pytest.mark.parametrize("kw,status", [
     ({"page": 20}, 2), ({"D": 80}, 2), ({"Hq": 5}, 2), ({"Hq": 0}, 2), ({"Hkv": 0}, 2), ({"qs": 255}, 2), ({"qs": 260}, 2),
-    ({"B": 8193}, 2), ({"B": -1}, 2), ({"T": -1}, 2), ({"max_pages": 0}, 2), ({"max_q": -1}, 2), ({"max_kv": -1}, 2),
+    ({"B": 8193}, 2), ({"B": -1}, 2), ({"T": -1}, 2), ({"max_pages": 0}, 2), ({"max_pages": (1 << 26) + 1}, 2), ({"T": 1 << 28}, 2), ({"max_q": -1}, 2), ({"max_kv": -1}, 2),
     ({"causal": 2}, 1), ({"window": -1}, 1), ({"causal": 0, "window": 4}, 1), ({"scale": 0.0}, 1), ({"scale": -1.0}, 1),
     ({"scale": math.inf}, 1), ({"scale": math.nan}, 1), ({"Q": None}, 1), ({"cu_q": None}, 1), ({"kv_lens": None}, 1),
     ({"table": None}, 1), ({"kcodes": None}, 1), ({"vscale": None}, 1), ({"O": None}, 1), ({"O": A + 8}, 1),
