@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(AttnCfg<D>::kWarps * 32, AttnCfg<D>::kCtas) kv
   };
 
   // A run's query rows (row g of each column tile), asked for ahead of its first tiles: behind them they would wait for
-  // everything that the whole GPU has just asked for.
+  // everything that the whole GPU has just asked for. (With two column tiles there are no registers to hold them.)
   uint32_t raw[NT][NK][2];
   auto queries = [&](const Run& r) {
 #pragma unroll
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(AttnCfg<D>::kWarps * 32, AttnCfg<D>::kCtas) kv
     }
   };
   open(run);
-  queries(run);
+  if constexpr (NT == 1) queries(run);
   fill(run);
   bool first_item = true;
   while (true) {
@@ -390,6 +390,7 @@ __global__ void __launch_bounds__(AttnCfg<D>::kWarps * 32, AttnCfg<D>::kCtas) kv
     // query fragments: row g of each column tile, scaled by a power of two into fp16
     uint32_t qf[NT][NK][2];
     float qs[NT][2];
+    if constexpr (NT > 1) queries(run);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       float amax = 0.f;
@@ -574,7 +575,7 @@ __global__ void __launch_bounds__(AttnCfg<D>::kWarps * 32, AttnCfg<D>::kCtas) kv
     __syncwarp();
     if (more) {
       open(next);
-      queries(next);
+      if constexpr (NT == 1) queries(next);
       fill(next);
     }
 

@@ -176,23 +176,27 @@ def hbl_quantize_qkv(X, T, H, d, bits, bos_token, codes, gamma, stream=None):
                                          _stream(stream)), "hbl_quantize_qkv")
 
 
+def _ptrs(*xs):
+    """``_ptr`` of several arguments (these calls take many, and a decode step is a few microseconds)."""
+    return [x if x is None or isinstance(x, int) else x.data_ptr() for x in xs]
+
+
 def hbl_kv_plan(new_lens, B, page, num_pages, max_pages, T, kv_lens, block_table, free_pages, free_count, cu_q, slots,
                 refused, stream=None):
-    return _check(lib().hbl_kv_plan(_ptr(new_lens), B, page, num_pages, max_pages, T, _ptr(kv_lens),
-                                    _ptr(block_table), _ptr(free_pages), _ptr(free_count), _ptr(cu_q), _ptr(slots),
-                                    _ptr(refused), _stream(stream)), "hbl_kv_plan")
+    new_lens, *rest = _ptrs(new_lens, kv_lens, block_table, free_pages, free_count, cu_q, slots, refused)
+    return _check(lib().hbl_kv_plan(new_lens, B, page, num_pages, max_pages, T, *rest, _stream(stream)), "hbl_kv_plan")
 
 
 def hbl_kv_append(K, V, T, Hkv, D, k_stride, v_stride, slots, page, num_pages, kcodes, vcodes, kscale, vscale,
                   stream=None):
-    return _check(lib().hbl_kv_append(_ptr(K), _ptr(V), T, Hkv, D, k_stride, v_stride, _ptr(slots), page, num_pages,
-                                      _ptr(kcodes), _ptr(vcodes), _ptr(kscale), _ptr(vscale), _stream(stream)),
-                  "hbl_kv_append")
+    K, V, slots, *cache = _ptrs(K, V, slots, kcodes, vcodes, kscale, vscale)
+    return _check(lib().hbl_kv_append(K, V, T, Hkv, D, k_stride, v_stride, slots, page, num_pages, *cache,
+                                      _stream(stream)), "hbl_kv_append")
 
 
 def hbl_kv_read(slots, T, Hkv, D, page, num_pages, kcodes, vcodes, kscale, vscale, K, V, stream=None):
-    return _check(lib().hbl_kv_read(_ptr(slots), T, Hkv, D, page, num_pages, _ptr(kcodes), _ptr(vcodes),
-                                    _ptr(kscale), _ptr(vscale), _ptr(K), _ptr(V), _stream(stream)), "hbl_kv_read")
+    slots, *rest = _ptrs(slots, kcodes, vcodes, kscale, vscale, K, V)
+    return _check(lib().hbl_kv_read(slots, T, Hkv, D, page, num_pages, *rest, _stream(stream)), "hbl_kv_read")
 
 
 def hbl_kv_attention_workspace_bytes(B: int, D: int) -> int:
@@ -202,10 +206,11 @@ def hbl_kv_attention_workspace_bytes(B: int, D: int) -> int:
 def hbl_kv_attention(Q, T, Hq, Hkv, D, q_stride, cu_q, kv_lens, B, max_q, max_kv, block_table, max_pages, page,
                      num_pages, kcodes, vcodes, kscale, vscale, scale, causal, window, O, lse, ws, ws_bytes,
                      stream=None):
-    return _check(lib().hbl_kv_attention(_ptr(Q), T, Hq, Hkv, D, q_stride, _ptr(cu_q), _ptr(kv_lens), B, max_q,
-                                         max_kv, _ptr(block_table), max_pages, page, num_pages, _ptr(kcodes),
-                                         _ptr(vcodes), _ptr(kscale), _ptr(vscale), scale, causal, window, _ptr(O),
-                                         _ptr(lse), _ptr(ws), ws_bytes, _stream(stream)), "hbl_kv_attention")
+    Q, cu_q, kv_lens, block_table, kc, vc, ks, vs, O, lse, ws = _ptrs(Q, cu_q, kv_lens, block_table, kcodes, vcodes,
+                                                                      kscale, vscale, O, lse, ws)
+    return _check(lib().hbl_kv_attention(Q, T, Hq, Hkv, D, q_stride, cu_q, kv_lens, B, max_q, max_kv, block_table,
+                                         max_pages, page, num_pages, kc, vc, ks, vs, scale, causal, window, O, lse,
+                                         ws, ws_bytes, _stream(stream)), "hbl_kv_attention")
 
 
 def hbl_selftest_wait_timeout(timeout_us, gave_up=None, stream=None):
