@@ -45,10 +45,17 @@ KvWs kv_ws_layout(int B, int D) {
   return L;
 }
 
-// Rows per key/value head up to which a request is streamed by kv_attn_kernel; more go to the tensor-core kernel.
+// Rows per key/value head up to which a request is streamed by kv_attn_kernel, two tiles of 16 that both read the
+// cache; more go to the tensor-core kernel, which reads it once for 256 rows but gives a request's head to one CTA.
 constexpr int kFewRows = 32;
 
-// Most cached tokens of a request, and most CTAs, for which kv_attn_kernel leaves each item to one CTA.
+// Rows of all query heads together up to which that holds for every request. Measured, tensor-core kernel / this one, us: 8
+// rows of 64 heads on 8 over 131072 keys (512 in all): 1771 / 231; 512 rows of 8 heads over 8192 (4096): 156 / 121; 64
+// rows of 32 over 32768 (2048): 457 / 240; 2048 rows of 4 over 2048 (8192): 50 / 78; 1024 rows of 8 over 1024 (8192): 28 / 31.
+constexpr int kFewInAll = 6144;
+
+// Most cached tokens of a request, and most CTAs, for which kv_attn_kernel leaves each item to one CTA: one request of 130
+// tokens, 32 heads of 128, takes 4.9 us so and 10.9 us with the parts joined by a second kernel.
 constexpr int kWholeKeys = 512, kWholeCtas = 4096;
 
 // Three kernels, each of which takes the requests that are its own: which those are is known on the GPU only.
@@ -75,8 +82,9 @@ int launch_kv_attention(const kv::AttnArgs& a, cudaStream_t s) {
   if (a.row_tiles == 0) {
     ProfScope ps("kv_combine", s);
     // few rows have many parts, many rows have few
-    const int rows = std::min(a.few_rows, a.most_rows);
-    const long long all = (long long)a.B * a.Hkv * rows;
+    const long long by_request = (long long)a.B * a.Hkv * std::min(a.few_rows, a.most_rows), by_token = (long long)a.T * a.Hq;
+    const int rows = by_request <= by_token ? std::min(a.few_rows, a.most_rows) : 0;
+    const long long all = std::min(by_request, by_token);
     if (all <= 256) launch_pdl(kv::kv_combine_kernel<D, 8>, dim3((unsigned)all), dim3(256), 0, s, a, rows);
     else if (all <= 1024) launch_pdl(kv::kv_combine_kernel<D, 2>, dim3((unsigned)((all + 3) / 4)), dim3(256), 0, s, a, rows);
     else launch_pdl(kv::kv_combine_kernel<D, 1>, dim3((unsigned)((all + 7) / 8)), dim3(256), 0, s, a, rows);
@@ -148,10 +156,12 @@ int hbl_kv_append(const hbl_bf16* K, const hbl_bf16* V, int T, int Hkv, int D, l
   if ((st = ensure_device(&d))) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const kv::AppendArgs a{K, V, k_stride, v_stride, kcodes, vcodes, kscale, vscale, slots, T, Hkv, ilog2(page), num_pages};
-  // Spans of a page (64 tokens at least) when there are many tokens, so that a run fills a block; shorter ones when the
-  // grid would else be smaller than two blocks for each place on the GPU.
+  // Spans of a page (64 tokens at least) when there are many tokens, so that a run fills a block; shorter ones, down to a
+  // token for each warp, until the grid has four blocks for each SM. Measured for other multiples (us, at 1 / 4 / 16): 8
+  // requests of 512 tokens, 8 heads of 128, pages of 128: 19.5 / 8.7 / 12.8; 7 of 300, 8 heads of 64, pages of 64: 5.3 /
+  // 5.1 / 8.8; 256 single tokens, 32 heads of 128: 16.5 / 11.3 / 11.9.
   int span = std::max(page, 64);
-  while (span > 8 && (long long)((T + span - 1) / span) * Hkv * 2 < 16ll * d->sm_count) span /= 2;
+  while (span > 8 && (long long)((T + span - 1) / span) * Hkv * 2 < 4ll * d->sm_count) span /= 2;
   const long long blocks = (long long)((T + span - 1) / span) * Hkv * 2;
   if (blocks >= (1ll << 31)) return HBL_ERR_SHAPE;
   const dim3 grid((unsigned)blocks);
@@ -222,6 +232,9 @@ int hbl_kv_attention(const hbl_bf16* Q, int T, int Hq, int Hkv, int D, long long
                        ilog2(page), num_pages, causal, window < max_pages * page ? window : 0,
                        std::min((D == 64 ? kv::AttnCfg<64>::kCtas : kv::AttnCfg<128>::kCtas) * d->sm_count, kv::kMaxAttnCtas), std::max(kFewRows, Hq / Hkv),
                        (int)std::min<long long>((long long)(max_q ? max_q : T) * (Hq / Hkv), 0x7fffffffll), 0, 0, 0, 0};
+  // The tensor-core kernel gives 256 rows of a head to one CTA for the whole length of their keys: with few such items most
+  // of the GPU would wait for them, and kv_attn_kernel, which splits the keys, takes every row.
+  if ((long long)T * Hq <= kFewInAll) a.few_rows = std::max(a.few_rows, a.most_rows);
   a.group_shift = ilog2(a.group);
   a.group_mul = (uint32_t)((((1ull << a.group_shift) - (uint64_t)a.group) << 32) / (uint64_t)a.group + 1);
   a.tile_rows = std::min(a.most_rows, a.few_rows) <= 8 ? 8 : 16;

@@ -83,7 +83,8 @@ struct PlanArgs {
 // new table entry and each page returned to the stack is found by itself with a binary search. A large step is taken by a
 // cluster of blocks: each forms the (short) sums for itself and takes its part of the rest; the lengths and the count,
 // which all of them read, are written behind a cluster barrier. Nothing here moves enough bytes to matter: it is bound
-// by its chain of dependent loads and barriers.
+// by its chain of dependent loads and barriers (4 requests of 5 rows: 4.4 us a step; 512 requests, 49 K rows: 10 us, by
+// one block 33 us).
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(PlanArgs a) {
   extern __shared__ int sm[];
   int* cu = sm;                       // [B + 1] first row of each request
@@ -325,7 +326,9 @@ HBL_DEVINL void append_run(const uint16_t* x, long long stride, int n, int off, 
 // A run is a row of tokens in consecutive slots of one page. A block takes the runs that begin in its span of
 // tokens, for one head's keys or values: a single long one with all its threads, several (or a short one) with a
 // warp each. It finds the run's absmax, raises the block's scale to it if it must (rescaling the codes that the
-// block held before the run), and writes the run's codes; the values are read once, for both.
+// block held before the run), and writes the run's codes; the values are read once, for both. The bound is HBM, two bytes
+// read and one written for each value: 8192 tokens, 32 heads of 128, pages of 64: 51 us, 3.9 TB/s (60 % of a copy;
+// reading them twice, a warp to a run: 235 us); 16 single tokens: 3.0 us.
 // HELD: 16-byte vectors that a thread holds, as many as a page gives it.
 template <int D, int HELD>
 __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const AppendArgs a, const int span) {
@@ -424,7 +427,7 @@ struct ReadArgs {
 constexpr int kReadItems = 4;         // vectors of 8 values of a thread
 
 // bf16((u - 128) * s), the product rounded to fp32 first. A thread's four 8-byte loads of codes are all
-// issued before the first is used.
+// issued before the first is used. Bound by HBM: 8192 tokens, 32 heads of 128: 33.9 us, 5.9 TB/s.
 template <int D>
 __global__ void __launch_bounds__(256) kv_read_kernel(const ReadArgs a) {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");

@@ -8,13 +8,19 @@
 //     values have the same layout: token rows of 64 channels; the keys are read K-major, the values MN-major);
 //   * warp 13 keeps the block scales a few tiles ahead;
 //   * warps 12 and 14, one for each half of the rows, issue tcgen05.mma kind::f16: S = Q K^T into TMEM, 64 keys a
-//     step, then O += P V with P as the A operand from TMEM;
+//     step (of which two are held), then O += P V with P as the A operand from TMEM;
 //   * warps 0..3 and 4..7 (a thread for each of 128 rows, twice) turn S into P in place. While one half's
 //     softmax runs, the tensor cores work for the other half: S, P and O of both fill the 512 TMEM columns.
 // A row's reference maximum is raised only when the running one has outgrown it by 2^8, and the values' reference
 // scale only when a block's scale is 16 times it, so the outputs in TMEM are rarely rescaled; probabilities
 // relative to such a reference stay below 2^12 and are rounded to fp16. A block's value scale enters as an addend of
 // the exponent (log2(s / reference)), which costs nothing; sums are fp32.
+// Measured: 2048-row chunks of four requests over up to 8192 keys, 32 query heads on 8 of 128: 710 us, 896 TFLOP/s (54 % of
+// the burst cuBLAS rate, 64 % of the sustained one, at 990 W); one prompt of 2048, 32 heads of their own: 67 us, of which
+// 9 us for each 256-row item are its beginning and end. A step of 64 keys takes 2280 cycles, of which the tensor cores work
+// 1264 (QK with N = 64 is bound by its shared-memory operands, 49 cycles an instruction) and the special function units 1024;
+// a scheduler has two softmax warps, a converting one and an issuing one, and what is left is their latencies:
+// without the exponentials the kernel would take 14 % less, without the maxima 10 %, without QK 8 %, without the loads 6 %.
 // Every wait is bounded, as in gemm_tc.cuh.
 #pragma once
 #include "gemm_tc.cuh"

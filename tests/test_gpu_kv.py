@@ -265,6 +265,15 @@ def check(L, case, **kw):
     return got, glse
 
 
+# Batches of up to 6144 rows of all heads go to the kernel that streams the keys, whatever their requests; more (rows
+# behind the last request count too) send a request of more than 32 rows a head to the tensor-core kernel.
+BOTH = pytest.mark.parametrize("many", [False, True])
+
+
+def spare(many, heads, least=0):
+    return 6144 // heads + 1 if many else least
+
+
 HEADS = [(4, 4, 128, 16), (8, 1, 64, 32), (6, 2, 128, 64), (16, 1, 128, 128), (3, 3, 64, 16), (40, 2, 64, 64)]
 
 
@@ -276,10 +285,11 @@ def test_attention_single_tokens(L, Hq, Hkv, D, page):
 
 @pytest.mark.parametrize("Hq,Hkv,D,page", HEADS)
 @pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 1), (True, 40)])
-def test_attention_ragged_rows(L, Hq, Hkv, D, page, causal, window):
+@BOTH
+def test_attention_ragged_rows(L, Hq, Hkv, D, page, causal, window, many):
     qs = [3, 0, 1, 17, 40, 5, 2, 8]
     kvs = [3, 9, 300, 17, 90, 2, 0, 140]      # 5 rows over 2 keys and 2 over none: rows that see nothing
-    check(L, make_case(L, 2, qs, kvs, Hq, Hkv, D, page, spare_rows=3), causal=causal, window=window)
+    check(L, make_case(L, 2, qs, kvs, Hq, Hkv, D, page, spare_rows=spare(many, Hq, 3)), causal=causal, window=window)
 
 
 @pytest.mark.parametrize("kv,Hq,Hkv,D,page", [(20011, 4, 1, 128, 16), (40000, 2, 2, 64, 64), (9973, 16, 1, 128, 128)])
@@ -290,16 +300,18 @@ def test_attention_long_context_is_split(L, kv, Hq, Hkv, D, page):
 
 @pytest.mark.parametrize("Hq,Hkv,D,page", [(4, 4, 128, 16), (4, 2, 64, 128), (8, 2, 128, 64), (5, 1, 128, 32)])
 @pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 100)])
-def test_attention_prompts(L, Hq, Hkv, D, page, causal, window):
-    check(L, make_case(L, 5, [200, 333, 1, 64], [200, 500, 77, 70], Hq, Hkv, D, page, spare_rows=2), causal=causal,
-          window=window)
+@BOTH
+def test_attention_prompts(L, Hq, Hkv, D, page, causal, window, many):
+    check(L, make_case(L, 5, [200, 333, 1, 64], [200, 500, 77, 70], Hq, Hkv, D, page, spare_rows=spare(many, Hq, 2)),
+          causal=causal, window=window)
 
 
 @pytest.mark.parametrize("Hq,Hkv,D,page", [(2, 1, 128, 16), (2, 2, 64, 32), (3, 1, 64, 128)])
 @pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 300)])
-def test_attention_long_prompts(L, Hq, Hkv, D, page, causal, window):
+@BOTH
+def test_attention_long_prompts(L, Hq, Hkv, D, page, causal, window, many):
     """More keys than any ring holds, more rows than a tile, block scales that keep outgrowing what came before."""
-    case = make_case(L, 15, [450, 130], [1500, 2049], Hq, Hkv, D, page, scale_spread=1.5)
+    case = make_case(L, 15, [450, 130], [1500, 2049], Hq, Hkv, D, page, spare(many, Hq), scale_spread=1.5)
     check(L, case, causal=causal, window=window)
     cache, Q, cu, kvs, table = case
     grow = torch.arange(table.shape[1], device="cuda", dtype=torch.float32)
@@ -310,9 +322,10 @@ def test_attention_long_prompts(L, Hq, Hkv, D, page, causal, window):
     check(L, case, causal=causal, window=window)
 
 
-def test_attention_prompts_of_all_scales(L):
+@BOTH
+def test_attention_prompts_of_all_scales(L, many):
     """Zero scales, and first tiles that a row does not see at all."""
-    case = make_case(L, 16, [300, 100, 90], [300, 60, 0], 2, 1, 128, 32)      # the last has no key at all
+    case = make_case(L, 16, [300, 100, 90], [300, 60, 0], 2, 1, 128, 32, spare(many, 2))      # the last has no key at all
     check(L, case)
     case[0].vscale[:] = 0
     check(L, case)
@@ -332,13 +345,14 @@ def test_attention_rows_beyond_the_bound_are_left(L):
     assert torch.equal(out[:2], cache.attention(Q, i32(cu), i32(kvs), i32(table))[:2])
 
 
-def test_attention_widest_window_and_rows(L):
+@BOTH
+def test_attention_widest_window_and_rows(L, many):
     """A window as wide as an int and more rows than keys: no limit of the kernels' own shows."""
-    case = make_case(L, 18, [5, 300], [2, 100], 2, 1, 64, 16)
+    case = make_case(L, 18, [5, 300], [2, 100], 2, 1, 64, 16, spare(many, 2))
     cache, Q, cu, kvs, table = case
     want = check(L, case)
     got = cache.attention(Q, i32(cu), i32(kvs), i32(table), window=2 ** 31 - 1, return_lse=True)
-    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    assert torch.equal(want[0][:305], got[0][:305]) and torch.equal(want[1][:305], got[1][:305])
 
 
 @pytest.mark.parametrize("kvs", [[130], [512, 1, 0], [513, 40, 33]])
@@ -376,8 +390,9 @@ def test_layer_refuses(L):
             bad()
 
 
-def test_attention_hints_do_not_change_results(L):
-    case = make_case(L, 6, [1, 4, 150], [100, 900, 400], 8, 2, 128, 32)
+@BOTH
+def test_attention_hints_do_not_change_results(L, many):
+    case = make_case(L, 6, [1, 4, 150], [100, 900, 400], 8, 2, 128, 32, spare(many, 8))
     got = [check(L, case, **kw) if not kw else case[0].attention(case[1], i32(case[2]), i32(case[3]), i32(case[4]),
                                                                  return_lse=True, **kw)
            for kw in ({}, {"max_q": 150, "max_kv": 900})]
@@ -450,17 +465,19 @@ def test_attention_what_is_masked_has_no_influence(L):
     assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
-def test_attention_odd_queries(L):
+@pytest.mark.parametrize("rows", [4, 80])      # 80 of them, and padding: the tensor-core kernel
+def test_attention_odd_queries(L, rows):
     """A NaN or an infinity in one row stays in that row; a row of zeros averages the values."""
-    case = make_case(L, 10, [4], [200], 2, 1, 64, 32)
+    case = make_case(L, 10, [rows], [200], 2, 1, 64, 32, spare(rows > 32, 2))
     cache, Q, cu, kvs, table = case
     Q[1, 0, 3] = float("nan")
     Q[2, 1, 5] = float("inf")
     Q[3, 0] = 0
     out, lse = cache.attention(Q, i32(cu), i32(kvs), i32(table), return_lse=True)
-    bad = torch.zeros(4, 2, dtype=torch.bool, device="cuda")
+    bad = torch.zeros(len(Q), 2, dtype=torch.bool, device="cuda")
     bad[1, 0] = bad[2, 1] = True
-    assert out[~bad].isfinite().all() and lse[~bad].isfinite().all()
+    good = ~bad & (torch.arange(len(Q), device="cuda") < rows)[:, None]
+    assert out[good].isfinite().all() and lse[good].isfinite().all()
     assert out[1, 0].isnan().all() and lse[1, 0].isnan()
     clean = Q.clone()
     clean[1, 0, 3] = 0
@@ -483,12 +500,13 @@ def test_attention_query_as_part_of_a_projection(L):
 def test_bad_pages_and_slots_are_skipped_and_recorded(L):
     from hadamard_bit_quant_b200 import hbl
     assert hbl.hbl_get_device_error() == 0
-    case = make_case(L, 13, [1, 2], [100, 200], 4, 2, 128, 16)
-    cache, Q, cu, kvs, table = case
-    table[0, 2], table[1, 5], table[1, 0] = -1, cache.num_pages, 2 ** 31 - 1
-    check(L, case)
-    assert hbl.hbl_get_device_error() == 1
-    assert hbl.hbl_get_device_error() == 0
+    for rows, pad in ((2, 0), (90, 1600)):                    # the streaming kernel, the tensor-core kernel
+        case = make_case(L, 13, [1, rows], [100, 200], 4, 2, 128, 16, pad)
+        cache, Q, cu, kvs, table = case
+        table[0, 2], table[1, 5], table[1, 0] = -1, cache.num_pages, 2 ** 31 - 1
+        check(L, case)
+        assert hbl.hbl_get_device_error() == 1
+        assert hbl.hbl_get_device_error() == 0
     before = [x.clone() for x in (cache.kcodes, cache.vcodes, cache.kscale, cache.vscale)]
     x = torch.randn(2, 2, 128, device="cuda").to(torch.bfloat16)
     cache.append(x, x, i32([cache.num_pages * 16, 2 ** 31 - 1]))
@@ -499,7 +517,7 @@ def test_bad_pages_and_slots_are_skipped_and_recorded(L):
     assert hbl.hbl_get_device_error() == 1
     assert bool((K[0] == 0).all())
     # lengths beyond the table and rows beyond the queries are cut
-    out = cache.attention(Q, i32([0, 1, 900]), i32([2 ** 30, -5]), i32(np.abs(table) % cache.num_pages))
+    out = cache.attention(Q, i32([0, 1, 9000]), i32([2 ** 30, -5]), i32(np.abs(table) % cache.num_pages))
     assert out[0].isfinite().all() and bool((out[1:] == 0).all())
 
 
