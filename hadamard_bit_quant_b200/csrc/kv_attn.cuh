@@ -158,7 +158,7 @@ HBL_DEVINL float exp2_fast(float x) {
 // The power of two that brings a row's largest magnitude into [2^14, 2^15), and its inverse.
 HBL_DEVINL void row_power(float amax, float* up, float* down) {
   int e = (int)(__float_as_uint(amax) >> 23) - 127;       // exponent; -127 for zero and subnormals
-  e = min(max(e, -100), 120);
+  e = min(max(e, -100), 127);
   *up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
   *down = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
 }

@@ -354,8 +354,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       const uint32_t sc0 = tc::su32(&S.scale[(j - lo) % kPreRing][0]);
       const float vnow = lds32f(sc0 + 96);
       const uint32_t bad = (__float_as_uint(lds32f(sc0 + 100)) >> (kPreStepGroups * (n & 1))) & 15u;
-      const float f[4] = {__uint_as_float(kq.x) * qs, __uint_as_float(kq.y) * qs, __uint_as_float(kq.z) * qs,
-                          __uint_as_float(kq.w) * qs};
+      // never zero, so that a masked score (minus infinity) stays one when it is multiplied
+      const float least = 1.17549435e-38f;
+      const float f[4] = {fmaxf(__uint_as_float(kq.x) * qs, least), fmaxf(__uint_as_float(kq.y) * qs, least),
+                          fmaxf(__uint_as_float(kq.z) * qs, least), fmaxf(__uint_as_float(kq.w) * qs, least)};
       const float add[4] = {__uint_as_float(vq.x), __uint_as_float(vq.y), __uint_as_float(vq.z), __uint_as_float(vq.w)};
       const float back[4] = {__uint_as_float(iq.x), __uint_as_float(iq.y), __uint_as_float(iq.z), __uint_as_float(iq.w)};
       tc::tc_wait_ld();
@@ -617,8 +619,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       }
     } else if (warp == 13) {
       // ----- block scales -----
-      // Lane g < 8 holds those of group g. The key scale of a group that no row sees is 1, and none is below the
-      // smallest that appending gives, so that a masked score (minus infinity) stays one when it is multiplied.
+      // Lane g < 8 holds those of group g. The key scale of a group that no row sees is 1, whatever its page has.
       const int32_t* table = a.table + (size_t)b * a.max_pages;
       const int any_first = a.window > 0 ? max(rq.kv - rq.q + by_group(a, row0) + 1 - a.window, 0) : 0;
       float ks = 1.f, vs = 0.f, vref = 0.f;
@@ -651,7 +652,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         // the probabilities of tile n - 4, its last user
         if (lane < kPreGroups) {
           float* dst = S.scale[n % kPreRing];
-          dst[lane] = fmaxf(ks, kScaleFloor);
+          dst[lane] = ks;
           dst[8 + lane] = lv;
           dst[16 + lane] = exp2_fast(-lv);
           if (lane == 0) {

@@ -407,9 +407,10 @@ def test_attention_many_requests(L):
     check(L, make_case(L, 7, rng.integers(0, 3, 700), kvs, 2, 1, 64, 16))
 
 
-def test_attention_scales_of_all_sizes(L):
-    """Block scales from 2^-60 to 2^40 side by side, queries from 1e-30 to 1e30."""
-    case = make_case(L, 8, [1, 1], [500, 90], 4, 2, 128, 16)
+@BOTH
+def test_attention_scales_of_all_sizes(L, many):
+    """Block scales from 2^-60 to 2^40 side by side, queries from 1e-30 to 3e38."""
+    case = make_case(L, 8, [40, 1] if many else [1, 1], [500, 90], 4, 2, 128, 16, spare(many, 4))
     cache, Q = case[0], case[1]
     rng = np.random.default_rng(5)
     cache.vscale.copy_(torch.tensor(2.0 ** rng.integers(-60, 40, cache.vscale.shape), dtype=torch.float32))
@@ -423,6 +424,9 @@ def test_attention_scales_of_all_sizes(L):
     Q.copy_((Q.float() * 1e30).to(torch.bfloat16))
     Q.mul_(1e30)
     check(L, case)
+    Q.mul_(3e7).clamp_(-3e38, 3e38)
+    Q[0, 0, :40] = 3e38
+    check(L, case, scale=2.0 ** -27)
 
 
 def test_cache_beyond_32_bit_offsets(L):
