@@ -5,6 +5,7 @@ is in libhbl's kernels.
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
 from functools import lru_cache
 from typing import NamedTuple
 
@@ -97,6 +98,14 @@ def _index(*tensors):
         assert x.get_device() == dev and x.dtype is torch.int32 and x.is_contiguous()
 
 
+def _allocating(stream):
+    """Context in which a call's own tensors are allocated: on the stream that it runs on, so that memory which it frees
+    at its end (a workspace) is not handed to another stream before it is through."""
+    if stream is None:
+        return nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 class KVPages:
     """Lengths, block table and free pages of a batch, shared by the caches of all layers.
 
@@ -107,7 +116,7 @@ class KVPages:
     def __init__(self, kv_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
                  free_count: torch.Tensor, page: int):
         _index(kv_lens, block_table, free_pages, free_count)
-        assert block_table.dim() == 2 and block_table.shape[0] == kv_lens.numel() and free_count.numel() == 1
+        assert block_table.dim() == 2 and block_table.shape[0] == kv_lens.numel() > 0 and free_count.numel() == 1
         self.kv_lens, self.block_table = kv_lens, block_table
         self.free_pages, self.free_count, self.page = free_pages, free_count, page
 
@@ -125,7 +134,8 @@ class KVPages:
         B, max_pages = self.block_table.shape
         assert new_lens.numel() == B
         if out is None:
-            out = KVStep(*new_lens.new_empty(tokens + 2 * B + 1).split_with_sizes((tokens, B + 1, B)))
+            with _allocating(stream):
+                out = KVStep(*new_lens.new_empty(tokens + 2 * B + 1).split_with_sizes((tokens, B + 1, B)))
         else:
             _index(*out)
             assert out.slots.numel() == tokens and out.cu_q.numel() == B + 1 and out.refused.numel() == B
@@ -185,7 +195,8 @@ class KVCache:
         _index(slots)
         assert slots.get_device() == self.kcodes.get_device()
         T = slots.numel()
-        K, V = self.kcodes.new_empty((2, T, self.kv_heads, self.head_dim), dtype=torch.bfloat16)
+        with _allocating(stream):
+            K, V = self.kcodes.new_empty((2, T, self.kv_heads, self.head_dim), dtype=torch.bfloat16)
         hbl.hbl_kv_read(slots, T, self.kv_heads, self.head_dim, self.page, self.num_pages, self.kcodes, self.vcodes,
                         self.kscale, self.vscale, K, V, stream)
         return K, V
@@ -208,19 +219,20 @@ class KVCache:
         T, Hq, D = Q.shape
         B, max_pages = block_table.shape
         assert kv_lens.numel() == B and cu_q.numel() == B + 1 and kv_lens.get_device() == self.kcodes.get_device()
-        if out is None:
-            out = Q.new_empty(T, Hq, D)
-        else:
+        if out is not None:
             assert out.shape == Q.shape and out.is_contiguous() and self._rows(out) == Hq * D
         if lse is not None:
             assert lse.shape == (T, Hq) and lse.dtype is torch.float32 and lse.is_contiguous()
             assert lse.get_device() == Q.get_device()
-        elif return_lse:
-            lse = self.kscale.new_empty(T, Hq)
-        if ws is None:
-            ws = self.workspace(B)
-        else:
+        if ws is not None:
             assert ws.dtype is torch.uint8 and ws.get_device() == Q.get_device()
+        with _allocating(stream):
+            if out is None:
+                out = Q.new_empty(T, Hq, D)
+            if lse is None and return_lse:
+                lse = self.kscale.new_empty(T, Hq)
+            if ws is None:
+                ws = self.workspace(B)
         hbl.hbl_kv_attention(Q, T, Hq, self.kv_heads, D, stride, cu_q, kv_lens, B, max_q, max_kv, block_table,
                              max_pages, self.page, self.num_pages, self.kcodes, self.vcodes, self.kscale, self.vscale,
                              D ** -0.5 if scale is None else scale, int(causal), window, out, lse, ws,

@@ -307,7 +307,7 @@ int hbl_quantize_qkv(const hbl_bf16* X, int T, int H, int d, int bits, int bos_t
  *                pages ran out, then also for every later request that needs
  *                a page). A refused request keeps its length and pages; its
  *                rows in cu_q are of no use to attention.
- * Requests of one batch share no page that this step writes.
+ * Requests of one batch share no page that this step writes. B = 0 writes nothing.
  */
 int hbl_kv_plan(const int32_t* new_lens, int B, int page, int num_pages, int max_pages, int T,
                 int32_t* kv_lens, int32_t* block_table, int32_t* free_pages, int32_t* free_count,

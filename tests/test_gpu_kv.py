@@ -624,3 +624,35 @@ def test_two_streams_with_workspaces_of_their_own(L):
                 outs.append(cache.attention(Q, *args, ws=cache.workspace(4)))
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_allocations_belong_to_the_stream_of_the_call(L, monkeypatch, handle):
+    """A call on another stream than the current one frees its workspace when it returns: that memory must stay with its
+    stream."""
+    case = make_case(L, 15, [1] * 4, [3000, 200, 5000, 1], 8, 2, 128, 64)
+    cache, Q, cu, kvs, table = case
+    args = i32(cu), i32(kvs), i32(table)
+    want = cache.attention(Q, *args, return_lse=True)
+    slots = torch.arange(100, dtype=torch.int32, device="cuda")
+    values = cache.read(slots)
+    seen, call = [], L.hbl.hbl_kv_attention
+    monkeypatch.setattr(L.hbl, "hbl_kv_attention", lambda *a: seen.append(a[-3].data_ptr()) or call(*a))
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    on = s.cuda_stream if handle else s
+    got = cache.attention(Q, *args, return_lse=True, stream=on)
+    again = cache.workspace(4)
+    assert seen and again.data_ptr() != seen[0]
+    read = cache.read(slots, stream=on)
+    pages, new = L.KVPages.empty(3, 4, 12, 16), i32([5, 0, 17])
+    torch.cuda.synchronize()
+    step = pages.plan(new, 22, stream=on)
+    s.synchronize()
+    assert all(torch.equal(g, w) for g, w in zip((*got, *read), (*want, *values)))
+    assert step.cu_q.tolist() == [0, 5, 5, 22] and step.slots.tolist()[:6] == [0, 1, 2, 3, 4, 16]
+
+
+def test_a_batch_has_a_request(L):
+    with pytest.raises(AssertionError):
+        L.KVPages.empty(0, 4, 8, 16)
