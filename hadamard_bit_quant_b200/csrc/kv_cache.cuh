@@ -83,7 +83,7 @@ struct PlanArgs {
 // new table entry and each page returned to the stack is found by itself with a binary search. A large step is taken by a
 // cluster of blocks: each forms the (short) sums for itself and takes its part of the rest; the lengths and the count,
 // which all of them read, are written behind a cluster barrier. Nothing here moves enough bytes to matter: it is bound
-// by its chain of dependent loads and barriers (4 requests of 5 rows: 4.4 us a step; 512 requests, 49 K rows: 10 us, by
+// by its chain of dependent loads and barriers (4 requests of 5 rows: 3.7 us a step; 512 requests, 49 K rows: 10 us, by
 // one block 33 us).
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(PlanArgs a) {
   extern __shared__ int sm[];
