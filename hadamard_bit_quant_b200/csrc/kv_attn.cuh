@@ -83,7 +83,7 @@ HBL_DEVINL Request request_of(const AttnArgs& a, int b) {
   r.q = min(max(a.cu_q[b + 1], r.row0), a.T) - r.row0;
   r.kv = (int)min((long long)max(a.kv_lens[b], 0), (long long)a.max_pages << a.page_log2);
   r.few = (long long)r.q * a.group <= a.few_rows;
-  r.rt = (int)(((long long)r.q * a.group + a.tile_rows - 1) / a.tile_rows);
+  r.rt = (r.q * a.group + a.tile_rows - 1) >> (a.tile_rows == 8 ? 3 : 4);
   // tiles from the first key that any of its rows sees to the last
   r.lo = a.window > 0 ? max(r.kv - r.q + 1 - a.window, 0) / kAttnTile : 0;
   r.tiles = r.q > 0 && r.few ? (r.kv + kAttnTile - 1) / kAttnTile - r.lo : 0;
@@ -287,19 +287,28 @@ __global__ void __launch_bounds__(AttnCfg<D>::kWarps * 32, AttnCfg<D>::kCtas) kv
   float* merge = reinterpret_cast<float*>(smem + C::kRing);                        // [warp][4][D], chunks permuted
   float2* merge_ml = reinterpret_cast<float2*>(smem + C::kRing + C::kMerge);       // [warp][8 NT]
 
-  // The run that begins at tile `at` of request r.b.
+  // The run that begins at tile `at` of request run.b; every other one is an item from its beginning.
+  auto take = [&](Run& r) {
+    r.hi = (int)min((long long)r.rq.tiles, r.lo + left);
+    left -= r.hi - r.lo;
+  };
   auto open = [&](Run& r) {
-    while (at >= tiles_of(a, r.rq)) {   // the next request with any tiles
-      at = 0;
-      r.rq = request_of(a, ++r.b);
-    }
     const int item = (int)(at / r.rq.tiles);
     r.lo = (int)(at % r.rq.tiles);
     r.h = item / r.rq.rt;
     r.rt = item % r.rq.rt;
-    r.hi = (int)min((long long)r.rq.tiles, r.lo + left);
-    at += r.hi - r.lo;
-    left -= r.hi - r.lo;
+    take(r);
+  };
+  auto open_next = [&](Run& r) {
+    r.lo = 0;
+    if (++r.rt == r.rq.rt) {
+      r.rt = 0;
+      if (++r.h == a.Hkv) {
+        r.h = 0;
+        do r.rq = request_of(a, ++r.b); while (r.rq.tiles == 0);    // the next request with any tiles
+      }
+    }
+    take(r);
   };
 
   // Copies of one tile: 32 token rows of keys and of values, and the scales of its (at most two) pages. Rows behind
@@ -578,7 +587,7 @@ __global__ void __launch_bounds__(AttnCfg<D>::kWarps * 32, AttnCfg<D>::kCtas) kv
     cp_wait<0>();
     __syncwarp();
     if (more) {
-      open(next);
+      open_next(next);
       if constexpr (NT == 1) queries(next);
       fill(next);
     }
