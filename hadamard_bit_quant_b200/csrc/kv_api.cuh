@@ -226,12 +226,13 @@ int hbl_kv_attention(const hbl_bf16* Q, int T, int Hq, int Hkv, int D, long long
   DeviceState* d = nullptr;
   if ((st = ensure_device(&d))) return st;
   uint8_t* w = static_cast<uint8_t*>(ws);
+  const int most_q = max_q > 0 && max_q < T ? max_q : T;    // no request has more than all: rows of a head then stay below 2^30
   kv::AttnArgs a{Q, q_stride, cu_q, kv_lens, block_table, kcodes, vcodes, kscale, vscale, O, lse,
                        reinterpret_cast<long long*>(w + L.prefix), reinterpret_cast<float*>(w + L.ml),
                        reinterpret_cast<float*>(w + L.o), scale * kv::kLog2e, T, Hq, Hkv, Hq / Hkv, B, max_pages,
                        ilog2(page), num_pages, causal, window < max_pages * page ? window : 0,
                        std::min((D == 64 ? kv::AttnCfg<64>::kCtas : kv::AttnCfg<128>::kCtas) * d->sm_count, kv::kMaxAttnCtas), std::max(kFewRows, Hq / Hkv),
-                       (int)std::min<long long>((long long)(max_q ? max_q : T) * (Hq / Hkv), 0x7fffffffll), 0, 0, 0, 0};
+                       most_q * (Hq / Hkv), 0, 0, 0, 0};
   // The tensor-core kernel gives 256 rows of a head to one CTA for the whole length of their keys: with few such items most
   // of the GPU would wait for them, and kv_attn_kernel, which splits the keys, takes every row.
   if ((long long)T * Hq <= kFewInAll) a.few_rows = std::max(a.few_rows, a.most_rows);

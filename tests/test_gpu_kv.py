@@ -656,3 +656,20 @@ def test_allocations_belong_to_the_stream_of_the_call(L, monkeypatch, handle):
 def test_a_batch_has_a_request(L):
     with pytest.raises(AssertionError):
         L.KVPages.empty(0, 4, 8, 16)
+
+
+@pytest.mark.parametrize("B,Hkv,rows", [(24, 1, 17), (3, 8, 40), (1, 2, 1)])
+def test_attention_any_bound_on_the_rows(L, B, Hkv, rows):
+    """A bound beyond all rows, up to the widest int, is no bound: the same bits, over short contexts too."""
+    case = make_case(L, 22, [rows] * B, [512] * B, 2 * Hkv, Hkv, 64, 16, spare_rows=2)
+    cache, Q, cu, kvs, table = case
+    args, ref = (Q, i32(cu), i32(kvs), i32(table)), reference(*case)
+    for kw in ({}, {"max_kv": 512}):
+        want = cache.attention(*args, return_lse=True, **kw)
+        close(*want, ref, float(cache.vscale.max()), 512)
+        for max_q in (len(Q) - 1, len(Q), len(Q) + 1, 2 ** 27, 2 ** 31 - 1):
+            got = cache.attention(*args, return_lse=True, max_q=max_q, **kw)
+            if max_q < len(Q):                               # fewer row tiles: other parts, not other results
+                close(*got, ref, float(cache.vscale.max()), 512)
+            else:
+                assert all(torch.equal(g[:rows * B], w[:rows * B]) for g, w in zip(got, want))
