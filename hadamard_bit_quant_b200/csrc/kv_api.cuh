@@ -116,7 +116,8 @@ int hbl_kv_plan(const int32_t* new_lens, int B, int page, int num_pages, int max
   const kv::PlanArgs a{new_lens, kv_lens, block_table, free_pages, free_count, cu_q, slots, refused,
                        B, ilog2(page), num_pages, max_pages, T};
   const size_t smem = 4 * ((size_t)B + 1) * 4;
-  ensure_smem_attr(kv::kv_plan_kernel, smem);
+  // for the largest batch whatever this one is: the kernel's static arrays count too, so the limit is short of 48 KB
+  ensure_smem_attr(kv::kv_plan_kernel, 4 * ((size_t)kv::kMaxRequests + 1) * 4);
   // a thread for each request or row up to a block's 1024; beyond that a cluster of blocks shares the rows
   const int most = std::max(B, T), threads = most <= 128 ? 128 : most <= 512 ? 512 : kv::kPlanThreads;
   const int ctas = T > 2 * kv::kPlanThreads ? kv::kPlanCtas : 1;

@@ -673,3 +673,22 @@ def test_attention_any_bound_on_the_rows(L, B, Hkv, rows):
                 close(*got, ref, float(cache.vscale.max()), 512)
             else:
                 assert all(torch.equal(g[:rows * B], w[:rows * B]) for g, w in zip(got, want))
+
+
+@pytest.mark.parametrize("B", [3054, 3055, 3071, 8192])
+def test_plan_in_a_fresh_process(B):
+    """Batches about the size where the kernel's shared memory passes 48 KB, with no larger one before them."""
+    import os
+    import subprocess
+    import sys
+    code = f"""
+import torch
+from hadamard_bit_quant_b200 import layer
+pages = layer.KVPages.empty({B}, 1, {B}, 16)
+step = pages.plan(torch.ones({B}, dtype=torch.int32, device="cuda"), {B})
+assert int(step.refused.sum()) == 0 and int(pages.free_count) == 0
+assert torch.equal(step.slots.cpu(), 16 * torch.arange({B}, dtype=torch.int32))
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
