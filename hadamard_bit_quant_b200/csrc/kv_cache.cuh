@@ -157,7 +157,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(PlanArgs a) {
   };
   auto handed = [&](int i) { return i < R ? released(i) : a.free_pages[F - 1 - (i - R)]; };
 
-  for (int t = tid; t < a.T; t += threads) {
+  // indexes run in 32 bits without a sign: one step behind the last of 2^31 - 1 rows is no int
+  for (uint32_t i = tid; i < (uint32_t)a.T; i += threads) {
+    const int t = (int)i;
     int slot = -1;
     if (t < cu[a.B]) {
       const int b = find_row(cu, a.B, t), n = len[b];
@@ -170,14 +172,15 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(PlanArgs a) {
     }
     a.slots[t] = slot;
   }
-  for (int i = tid; i < used; i += threads) {
-    const int b = find_row(want, a.B, i);
+  for (uint32_t n = tid; n < (uint32_t)used; n += threads) {
+    const int i = (int)n, b = find_row(want, a.B, i);
     a.table[(size_t)b * a.max_pages + (size_t)(pages(len[b]) + (i - want[b]))] = handed(i);
   }
   // what was given back and not handed out again: the last of it lies deepest, so a step that is undone
   // leaves the stack as it was
-  for (int i = used + tid; i < R; i += threads) {
-    const int at = F + (R - 1 - i);
+  for (uint32_t n = (uint32_t)used + tid; n < (uint32_t)R; n += threads) {
+    const int i = (int)n;
+    const long long at = (long long)F + (R - 1 - i);
     if (at < a.num_pages) a.free_pages[at] = released(i);
     else set_device_error(HBL_ERR_INVALID_ARG);
   }

@@ -692,3 +692,17 @@ assert torch.equal(step.slots.cpu(), 16 * torch.arange({B}, dtype=torch.int32))
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr
+
+
+def test_plan_of_the_most_rows(L):
+    """As many rows as an int counts: each of them is written, and nothing but them."""
+    T = 2 ** 31 - 1
+    buf = torch.full((T + 64,), 7, dtype=torch.int32, device="cuda")
+    pages = L.KVPages.empty(2, 4, 8, 16)
+    step = L.KVStep(buf[:T], i32([0] * 3), i32([0] * 2))
+    pages.plan(i32([20, 3]), T, out=step)
+    assert step.cu_q.tolist() == [0, 20, 23] and step.refused.tolist() == [0, 0]
+    assert step.slots[:23].tolist() == list(range(20)) + [32, 33, 34]
+    assert bool((buf[T:] == 7).all())
+    for part in buf[23:T].split(2 ** 28):
+        assert int(part.max()) == int(part.min()) == -1
