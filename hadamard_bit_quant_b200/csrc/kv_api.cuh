@@ -82,8 +82,8 @@ int launch_kv_attention(const kv::AttnArgs& a, cudaStream_t s) {
   if (a.row_tiles == 0) {
     ProfScope ps("kv_combine", s);
     // few rows have many parts, many rows have few
-    const long long by_request = (long long)a.B * a.Hkv * std::min(a.few_rows, a.most_rows), by_token = (long long)a.T * a.Hq;
-    const int rows = by_request <= by_token ? std::min(a.few_rows, a.most_rows) : 0;
+    const long long by_request = (long long)a.B * a.Hkv * a.few_rows, by_token = (long long)a.T * a.Hq;
+    const int rows = by_request <= by_token ? a.few_rows : 0;
     const long long all = std::min(by_request, by_token);
     if (all <= 256) launch_pdl(kv::kv_combine_kernel<D, 8>, dim3((unsigned)all), dim3(256), 0, s, a, rows);
     else if (all <= 1024) launch_pdl(kv::kv_combine_kernel<D, 2>, dim3((unsigned)((all + 3) / 4)), dim3(256), 0, s, a, rows);
@@ -236,14 +236,15 @@ int hbl_kv_attention(const hbl_bf16* Q, int T, int Hq, int Hkv, int D, long long
                        most_q * (Hq / Hkv), 0, 0, 0, 0};
   // The tensor-core kernel gives 256 rows of a head to one CTA for the whole length of their keys: with few such items most
   // of the GPU would wait for them, and kv_attn_kernel, which splits the keys, takes every row.
-  if ((long long)T * Hq <= kFewInAll) a.few_rows = std::max(a.few_rows, a.most_rows);
+  if ((long long)T * Hq <= kFewInAll) a.few_rows = a.most_rows;
+  a.few_rows = std::min(a.few_rows, a.most_rows);           // a request beyond the caller's bound is nobody's
   a.group_shift = ilog2(a.group);
   a.group_mul = (uint32_t)((((1ull << a.group_shift) - (uint64_t)a.group) << 32) / (uint64_t)a.group + 1);
-  a.tile_rows = std::min(a.most_rows, a.few_rows) <= 8 ? 8 : 16;
+  a.tile_rows = a.few_rows <= 8 ? 8 : 16;
   // Few enough keys for one CTA to be through with them before a second kernel could have joined the parts: each item
   // is left whole (at most kWholeCtas of them, so that the grid stays a few waves).
   const long long most_kv = std::min<long long>(max_kv ? max_kv : 1ll << 40, (long long)max_pages * page);
-  const int row_tiles = (std::min(a.most_rows, a.few_rows) + a.tile_rows - 1) / a.tile_rows;
+  const int row_tiles = (a.few_rows + a.tile_rows - 1) / a.tile_rows;
   if (most_kv <= kWholeKeys && (long long)B * Hkv * row_tiles <= kWholeCtas) {
     a.row_tiles = row_tiles;
     a.ctas = B * Hkv * row_tiles;

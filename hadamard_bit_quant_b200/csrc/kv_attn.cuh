@@ -59,7 +59,7 @@ struct AttnArgs {
   float scale_log2;                   // softmax scale * log2(e)
   int T, Hq, Hkv, group, B, max_pages, page_log2, num_pages, causal, window, ctas;
   int few_rows;                       // requests with more rows per key/value head than this go to kv_prefill_kernel
-  int most_rows;                      // and those with more than this break the caller's bound
+  int most_rows;                      // (>= few_rows) and those with more than this break the caller's bound: no kernel's
   int tile_rows;                      // query rows that kv_attn_kernel takes at a time: 8 or 16
   uint32_t group_mul;                 // division by group: see by_group
   int group_shift;

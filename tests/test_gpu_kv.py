@@ -706,3 +706,23 @@ def test_plan_of_the_most_rows(L):
     assert bool((buf[T:] == 7).all())
     for part in buf[23:T].split(2 ** 28):
         assert int(part.max()) == int(part.min()) == -1
+
+
+@pytest.mark.parametrize("q", [5, 10])
+@pytest.mark.parametrize("kv,kw", [(300, {}), (300, {"max_kv": 512}), (20000, {})])
+@BOTH
+def test_attention_few_rows_beyond_the_bound_are_left(L, q, kv, kw, many):
+    """Rows beyond the bound that a kernel of few rows could take: left all the same, the other requests' are written."""
+    from hadamard_bit_quant_b200 import hbl
+    case = make_case(L, 23, [2, q, 1], [50, kv, 40], 4, 2, 64, 16, spare(many, 4), width=32 if kv < 500 else None)
+    cache, Q, cu, kvs, table = case
+    out, lse = torch.full_like(Q, 7.0), torch.full(Q.shape[:2], 7.0, device="cuda")
+    cache.attention(Q, i32(cu), i32(kvs), i32(table), max_q=2, out=out, lse=lse, return_lse=True, **kw)
+    assert hbl.hbl_get_device_error() == 1
+    left = slice(2, 2 + q)
+    assert bool((out[left] == 7).all()) and bool((lse[left] == 7).all())
+    kvs = kvs.copy()
+    kvs[1] = 0                                               # not compared, and quick
+    want = reference(cache, Q, cu, kvs, table)
+    want[1][left] = np.nan
+    close(out, lse, want, float(cache.vscale.max()), 50)
