@@ -31,7 +31,7 @@ int check_table(int B, int max_pages, int page) {
 }
 
 struct KvWs {
-  size_t prefix, ml, o, total;
+  size_t prefix, mz, o, total;
 };
 
 KvWs kv_ws_layout(int B, int D) {
@@ -39,7 +39,7 @@ KvWs kv_ws_layout(int B, int D) {
   size_t off = 0;
   const size_t rows = (size_t)kv::kMaxAttnCtas * 2 * kv::kAttnRows;
   L.prefix = off; off = align_up(off + ((size_t)B + 1) * 8, 256);
-  L.ml = off; off = align_up(off + rows * 8, 256);
+  L.mz = off; off = align_up(off + rows * 8, 256);
   L.o = off; off = align_up(off + rows * D * 4, 256);
   L.total = off;
   return L;
@@ -229,7 +229,7 @@ int hbl_kv_attention(const hbl_bf16* Q, int T, int Hq, int Hkv, int D, long long
   uint8_t* w = static_cast<uint8_t*>(ws);
   const int most_q = max_q > 0 && max_q < T ? max_q : T;    // no request has more than all: rows of a head then stay below 2^30
   kv::AttnArgs a{Q, q_stride, cu_q, kv_lens, block_table, kcodes, vcodes, kscale, vscale, O, lse,
-                       reinterpret_cast<long long*>(w + L.prefix), reinterpret_cast<float*>(w + L.ml),
+                       reinterpret_cast<long long*>(w + L.prefix), reinterpret_cast<float*>(w + L.mz),
                        reinterpret_cast<float*>(w + L.o), scale * kv::kLog2e, T, Hq, Hkv, Hq / Hkv, B, max_pages,
                        ilog2(page), num_pages, causal, window < max_pages * page ? window : 0,
                        std::min((D == 64 ? kv::AttnCfg<64>::kCtas : kv::AttnCfg<128>::kCtas) * d->sm_count, kv::kMaxAttnCtas), std::max(kFewRows, Hq / Hkv),

@@ -15,12 +15,14 @@
 //     two into fp16's range (exact but for what lies 2^-25 below the row's largest value), and both products
 //     run on mma.m16n8k16 with fp32 sums, the tokens (then the channels) as the 16 rows and the query rows as the 8
 //     columns: with 8 query rows nothing is padded, where a 128-row tcgen05 tile would be 15/16 padding;
-//   * a block's key scale multiplies the scores, its value scale the probabilities, relative to a reference value
-//     scale. Reference maximum and scale are raised only when a tile outgrows them by 2^8 and 16: then no
-//     lane has to ask the others for the tile's maximum. Probabilities stay below 2^12 and are rounded to fp16 (11
-//     bits), finer than the bf16 output.
-// At the end of a run the warps' results are added through shared memory. A run that is only a part of its
-// row's keys goes to the workspace, and kv_combine_kernel joins the parts.
+//   * a block's key scale multiplies the scores; its value scale s enters as an addend log2(s) of the exponent. So
+//     the second product takes weights p s, relative to a reference of their own row: nothing that a row does not see
+//     has a part in how they are rounded. The sum of the p, relative to a reference of the scores alone, is that of the
+//     weights times 1 / s. Both references are raised only when a tile outgrows the weights' by 2^8: then no lane has to ask
+//     the others for the tile's maxima. Weights stay below 2^8 and are rounded to fp16 (11 bits), finer than the bf16 output.
+// At the end of a run the warps' results are joined through shared memory: weighted values relative to the largest weights'
+// reference, and the log2 of the sums. A run that is only a part of its row's keys goes to the workspace in the same form,
+// and kv_combine_kernel joins the parts.
 // Measured, of HBM's copy rate on the codes, queries and outputs: 128 requests of up to 4096 tokens, 32 query heads on 8 of
 // 128: 143 us, 5.6 TB/s (86 %); one of 131072: 56 us, 4.8 TB/s (73 %); 16 of up to 2048, 32 heads each their own: 43 us,
 // 4.5 TB/s (69 %). What is left there is the start (lengths, table, first tiles: 4 us one after the other), the
@@ -35,8 +37,14 @@ namespace kv {
 
 constexpr int kAttnTile = 32;         // tokens of a warp's tile
 constexpr int kAttnRows = 16;         // most query rows of a tile
-constexpr float kLag = 8.f;           // log2 of how far a tile may outgrow the reference maximum
-constexpr float kSlack = 16.f;        // and a value scale the reference scale
+constexpr float kLag = 8.f;           // log2 of how far a tile may outgrow the reference
+// log2 of how far a block's value scale may lie below that of the row's largest weight before the scores' reference is brought
+// up to date (the sum, relative to it, stays below 2^104 for each key). With one that lies further below the block then counts
+// as that far: its weights are zero in fp16 either way, and the p that the sum gets back from them neither vanish nor
+// overflow. kLeastScale: log2 of the least value scale that is told apart (appending makes none below 2^-100); kZeroScale
+// stands for that of 0, which leaves the weights' reference as it is.
+constexpr float kSpread = 96.f, kLeastScale = -118.f, kZeroScale = -2e30f;
+constexpr float kNothing = -1e30f;    // references of a row that has seen no key
 constexpr int kMaxAttnCtas = 480;     // workspace is laid out for this many
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -54,8 +62,8 @@ struct AttnArgs {
   uint16_t* O;                        // T x Hq x D
   float* lse;                         // T x Hq or null
   long long* prefix;                  // workspace: tiles before each request, B + 1
-  float* part_ml;                     // workspace: [cta][2][16] maximum and sum
-  float* part_o;                      // workspace: [cta][2][16][D]
+  float* part_mz;                     // workspace: [cta][2][16] the weights' reference of a part and log2 of its sum
+  float* part_o;                      // workspace: [cta][2][16][D] weighted values relative to that reference
   float scale_log2;                   // softmax scale * log2(e)
   int T, Hq, Hkv, group, B, max_pages, page_log2, num_pages, causal, window, ctas;
   int few_rows;                       // requests with more rows per key/value head than this go to kv_prefill_kernel
@@ -155,6 +163,11 @@ HBL_DEVINL float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
+
+HBL_DEVINL float log2_scale(float s) { return s > 0.f ? fmaxf(__log2f(s), kLeastScale) : kZeroScale; }
+
+// 1 / l, and 0 for a row without keys.
+HBL_DEVINL float over(float l) { return l > 0.f || l != l ? __fdividef(1.f, l) : 0.f; }
 
 // The power of two that brings a row's largest magnitude into [2^14, 2^15), and its inverse.
 HBL_DEVINL void row_power(float amax, float* up, float* down) {
@@ -286,7 +299,7 @@ __global__ void __launch_bounds__(AttnCfg<D>::kWarps * 32, AttnCfg<D>::kCtas) kv
   uint8_t* ring = smem + warp * (C::kStages * C::kStageBytes);
   const uint32_t ring_u = (uint32_t)__cvta_generic_to_shared(ring);
   float* merge = reinterpret_cast<float*>(smem + C::kRing);                        // [warp][4][D], chunks permuted
-  float2* merge_ml = reinterpret_cast<float2*>(smem + C::kRing + C::kMerge);       // [warp][8 NT]
+  float2* merge_mz = reinterpret_cast<float2*>(smem + C::kRing + C::kMerge);       // [warp][8 NT]
 
   // The run that begins at tile `at` of request run.b; every other one is an item from its beginning, found without a
   // division (with four in 64 bits: 16 requests 45 us instead of 43, 2048 of 100 tokens 219 instead of 197).
@@ -430,14 +443,14 @@ __global__ void __launch_bounds__(AttnCfg<D>::kWarps * 32, AttnCfg<D>::kCtas) kv
     }
 
     // this thread's rows are 8 i + 2 t4 + e; output tile jj holds the channels 2 NJ g + 2 jj and the next one
-    float o[NT][NJ][4], m[NT][2], l[NT][2], vref = 0.f;
+    float o[NT][NJ][4], m[NT][2], ref[NT][2], l[NT][2];      // weights' reference, scores', and the sum relative to that
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
 #pragma unroll
       for (int jj = 0; jj < NJ; ++jj)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][jj][e] = 0.f;
-      m[i][0] = m[i][1] = -INFINITY;
+      m[i][0] = m[i][1] = ref[i][0] = ref[i][1] = kNothing;
       l[i][0] = l[i][1] = 0.f;
     }
 
@@ -471,7 +484,8 @@ __global__ void __launch_bounds__(AttnCfg<D>::kWarps * 32, AttnCfg<D>::kCtas) kv
             }
           }
         const float2 ks = lds64f(s0 + 2 * C::kKBytes);
-        float2 vs = lds64f(s0 + 2 * C::kKBytes + 8);
+        const float2 vs = lds64f(s0 + 2 * C::kKBytes + 8);
+        float lv[2] = {log2_scale(vs.x), log2_scale(vs.y)};
         const bool whole = key0 >= all_first && key0 + kAttnTile <= all_last && ks.x >= 0.f && ks.y >= 0.f;
 #pragma unroll
         for (int i = 0; i < NT; ++i)
@@ -497,57 +511,55 @@ __global__ void __launch_bounds__(AttnCfg<D>::kWarps * 32, AttnCfg<D>::kCtas) kv
                 }
             }
           // a half of which no row sees anything: its page's scale says nothing
-          if (key0 >= any_last || key0 + 16 <= any_first || ks.x < 0.f) vs.x = 0.f;
-          if (key0 + 16 >= any_last || key0 + 32 <= any_first || ks.y < 0.f) vs.y = 0.f;
+          if (key0 >= any_last || key0 + 16 <= any_first || !(ks.x >= 0.f)) lv[0] = lv[1];
+          if (key0 + 16 >= any_last || key0 + 32 <= any_first || !(ks.y >= 0.f)) lv[1] = lv[0];
         }
-        // references: raised when any lane's scores, or a value scale, have outgrown them
-        const float vmax = fmaxf(vs.x, vs.y);
-        bool grown = vmax > kSlack * vref;
-        float x[NT][2];
+        // references: raised when any lane's weights have outgrown them
+        auto addend = [&](int i, int e, int hh) { return fmaxf(lv[hh] - m[i][e], -ref[i][e] - kSpread); };
+        const float quiet = fminf(lv[0], lv[1]);
+        bool grown = false;
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            x[i][e] = fmaxf(fmaxf(s[i][0][e], s[i][0][e + 2]), fmaxf(s[i][1][e], s[i][1][e + 2]));
-            grown |= x[i][e] > m[i][e] + kLag;
+            const float s0 = fmaxf(s[i][0][e], s[i][0][e + 2]), s1 = fmaxf(s[i][1][e], s[i][1][e + 2]);
+            grown |= fmaxf(s0 + lv[0], s1 + lv[1]) > m[i][e] + kLag || quiet < m[i][e] - ref[i][e] - kSpread;
           }
         if (__any_sync(0xffffffffu, grown)) {
-          const float vnew = vmax > kSlack * vref ? vmax : vref;
-          const float shrink = vnew == vref ? 1.f : __fdividef(vref, vnew);
-          vref = vnew;
 #pragma unroll
           for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float y = x[i][e];
+              const float s0 = fmaxf(s[i][0][e], s[i][0][e + 2]), s1 = fmaxf(s[i][1][e], s[i][1][e + 2]);
+              float y = fmaxf(s0 + lv[0], s1 + lv[1]), ys = fmaxf(s0, s1);
 #pragma unroll
-              for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
-              const float mn = fmaxf(m[i][e], y);
-              const float alpha = mn == m[i][e] ? 1.f : exp2_fast(m[i][e] - mn);
+              for (int d = 4; d < 32; d <<= 1) {
+                y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+                ys = fmaxf(ys, __shfl_xor_sync(0xffffffffu, ys, d));
+              }
+              const float mn = fmaxf(m[i][e], y), rn = fmaxf(ref[i][e], ys);
+              const float alpha = exp2_fast(m[i][e] - mn);
+              l[i][e] *= exp2_fast(ref[i][e] - rn);
               m[i][e] = mn;
-              l[i][e] *= alpha;
+              ref[i][e] = rn;
 #pragma unroll
               for (int jj = 0; jj < NJ; ++jj) {
-                o[i][jj][e] *= alpha * shrink;
-                o[i][jj][e + 2] *= alpha * shrink;
+                o[i][jj][e] *= alpha;
+                o[i][jj][e + 2] *= alpha;
               }
             }
         }
-        const float inv = vref > 0.f ? __fdividef(1.f, vref) : 0.f;
-        const float vr[2] = {vs.x * inv, vs.y * inv};
         uint32_t pf[NT][2][2];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          const float mu[2] = {m[i][0] == -INFINITY ? 0.f : m[i][0], m[i][1] == -INFINITY ? 0.f : m[i][1]};
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
+            const float add[2] = {addend(i, 0, hh), addend(i, 1, hh)};
             float p[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              p[e] = exp2_fast(s[i][hh][e] - mu[e & 1]);
-              l[i][e & 1] += p[e];
-              p[e] *= vr[hh];
-            }
+            for (int e = 0; e < 4; ++e) p[e] = exp2_fast(s[i][hh][e] + add[e & 1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) l[i][e] = __fmaf_rn(p[e] + p[e + 2], exp2_fast(-ref[i][e] - add[e]), l[i][e]);
             // a token's two rows side by side; transposed, a row's two tokens
             pf[i][hh][0] = transpose8(pack_half(p[0], p[1]));
             pf[i][hh][1] = transpose8(pack_half(p[2], p[3]));
@@ -594,14 +606,14 @@ __global__ void __launch_bounds__(AttnCfg<D>::kWarps * 32, AttnCfg<D>::kCtas) kv
       fill(next);
     }
 
-    // add the warps' results
+    // join the warps' results
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], d);
-        if (g == 0) merge_ml[warp * 8 * NT + 8 * i + 2 * t4 + e] = make_float2(m[i][e], l[i][e]);
+        if (g == 0) merge_mz[warp * 8 * NT + 8 * i + 2 * t4 + e] = make_float2(m[i][e], ref[i][e] + __log2f(l[i][e]));
       }
     const bool final_ = run.lo == 0 && run.hi == rq.tiles;
     const size_t slot = ((size_t)blockIdx.x * 2 + (first_item ? 0 : 1)) * kAttnRows;
@@ -617,8 +629,7 @@ __global__ void __launch_bounds__(AttnCfg<D>::kWarps * 32, AttnCfg<D>::kCtas) kv
             const auto& u = o[pass >> 1][2 * c];
             const auto& w = o[pass >> 1][2 * c + 1];
             const int ch = (NJ / 2) * g + c;                // chunk of four channels, moved by the row pair
-            *reinterpret_cast<float4*>(dst + 4 * (ch ^ (t4 & 1))) =
-                make_float4(u[e] * vref, u[e + 2] * vref, w[e] * vref, w[e + 2] * vref);
+            *reinterpret_cast<float4*>(dst + 4 * (ch ^ (t4 & 1))) = make_float4(u[e], u[e + 2], w[e], w[e + 2]);
           }
         }
       }
@@ -626,17 +637,20 @@ __global__ void __launch_bounds__(AttnCfg<D>::kWarps * 32, AttnCfg<D>::kCtas) kv
       for (int i = threadIdx.x; i < D; i += blockDim.x) {   // 4 rows x D / 4 chunks
         const int rr = i / (D / 4), ch = i % (D / 4), r = 4 * pass + rr;
         if (r < rows) {
-          float M = -INFINITY, L = 0.f;
+          float M = kNothing, Z = -INFINITY, L = 0.f;
 #pragma unroll
-          for (int k = 0; k < kAttnWarps; ++k) M = fmaxf(M, merge_ml[k * 8 * NT + r].x);
-          const float mu = M == -INFINITY ? 0.f : M;
+          for (int k = 0; k < kAttnWarps; ++k) {
+            M = fmaxf(M, merge_mz[k * 8 * NT + r].x);
+            Z = fmaxf(Z, merge_mz[k * 8 * NT + r].y);
+          }
+          Z = Z == -INFINITY ? 0.f : Z;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int k = 0; k < kAttnWarps; ++k) {
-            const float2 ml = merge_ml[k * 8 * NT + r];
-            const float f = exp2_fast(ml.x - mu);
+            const float2 mz = merge_mz[k * 8 * NT + r];
+            const float f = exp2_fast(mz.x - M);
             const float4 v = *reinterpret_cast<const float4*>(merge + (k * 4 + rr) * D + 4 * (ch ^ (rr >> 1)));
-            L += ml.y * f;
+            L += exp2_fast(mz.y - Z);
             acc.x += v.x * f; acc.y += v.y * f; acc.z += v.z * f; acc.w += v.w * f;
           }
           const int d = 4 * ch;
@@ -644,18 +658,15 @@ __global__ void __launch_bounds__(AttnCfg<D>::kWarps * 32, AttnCfg<D>::kCtas) kv
             const int row = row_lo + r;
             const int tok = by_group(a, row);
             const size_t out = (size_t)(rq.row0 + tok) * a.Hq + (size_t)(run.h * a.group + row - tok * a.group);
-            const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+            const float root = exp2_fast(0.5f * (M - Z)), inv = root * over(L);   // 2^(M - Z) itself may have no place in fp32
             uint2 y;
-            y.x = (uint32_t)float_to_bf16_bits(acc.x * inv) | ((uint32_t)float_to_bf16_bits(acc.y * inv) << 16);
-            y.y = (uint32_t)float_to_bf16_bits(acc.z * inv) | ((uint32_t)float_to_bf16_bits(acc.w * inv) << 16);
+            y.x = (uint32_t)float_to_bf16_bits(acc.x * inv * root) | ((uint32_t)float_to_bf16_bits(acc.y * inv * root) << 16);
+            y.y = (uint32_t)float_to_bf16_bits(acc.z * inv * root) | ((uint32_t)float_to_bf16_bits(acc.w * inv * root) << 16);
             *reinterpret_cast<uint2*>(a.O + out * D + d) = y;
-            if (a.lse && ch == 0) a.lse[out] = L > 0.f || L != L ? M * kLn2 + logf(L) : -INFINITY;
+            if (a.lse && ch == 0) a.lse[out] = L == 0.f ? -INFINITY : Z * kLn2 + logf(L);
           } else {
             *reinterpret_cast<float4*>(a.part_o + (slot + r) * D + d) = acc;
-            if (ch == 0) {
-              a.part_ml[2 * (slot + r)] = M;
-              a.part_ml[2 * (slot + r) + 1] = L;
-            }
+            if (ch == 0) *reinterpret_cast<float2*>(a.part_mz + 2 * (slot + r)) = make_float2(M, Z + __log2f(L));
           }
         }
       }
@@ -675,7 +686,8 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const AttnArgs a, const
   constexpr int V = D / 32;                                 // channels of a lane
   constexpr int kPer = 8 / KW;                              // rows of a block
   __shared__ float s_acc[kPer][KW][D];
-  __shared__ float2 s_ml[kPer][KW];
+  __shared__ float2 s_mz[kPer][KW];
+  __shared__ float s_l[kPer][KW];
   const int lane = threadIdx.x & 31, k = (threadIdx.x >> 5) % KW, half = threadIdx.x / (32 * KW);
   const long long i = (long long)blockIdx.x * kPer + half;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
@@ -701,7 +713,7 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const AttnArgs a, const
     mine = mine && r >= 0;
   }
   size_t row = 0;
-  float M = -INFINITY, L = 0.f, acc[V] = {};
+  float M = kNothing, Z = -INFINITY, L = 0.f, acc[V] = {};   // weighted values relative to 2^M, sum relative to 2^Z
   if (mine) {
     const Request rq = request_of(a, b);
     if (r == 0 && h == 0 && k == 0 && lane == 0) check_bound(a, rq);
@@ -719,32 +731,34 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const AttnArgs a, const
         // the first part is its CTA's last item, unless the CTA begins with it; every other one is its CTA's first
         const int tail = total * c0 / n != x0;
         for (int c = c0 + k; c <= c1; c += 4 * KW) {        // four parts at a time, all asked for before the first is used
-          float2 ml[4];
+          float2 mz[4];
           float v[4][V];
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
             const int at = c + p * KW;
-            ml[p] = make_float2(-INFINITY, 0.f);
+            mz[p] = make_float2(kNothing, -INFINITY);
 #pragma unroll
             for (int e = 0; e < V; ++e) v[p][e] = 0.f;
             if (at <= c1) {
               const size_t slot = ((size_t)at * 2 + (at == c0 ? tail : 0)) * kAttnRows + r % a.tile_rows;
-              ml[p] = *reinterpret_cast<const float2*>(a.part_ml + 2 * slot);
+              mz[p] = *reinterpret_cast<const float2*>(a.part_mz + 2 * slot);
               const float* o = a.part_o + slot * D + V * lane;
               if constexpr (V == 4) *reinterpret_cast<float4*>(v[p]) = *reinterpret_cast<const float4*>(o);
               else *reinterpret_cast<float2*>(v[p]) = *reinterpret_cast<const float2*>(o);
             }
           }
-          const float mn = fmaxf(M, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
-          const float mu = mn == -INFINITY ? 0.f : mn, f0 = exp2_fast(M - mu);
+          const float mn = fmaxf(M, fmaxf(fmaxf(mz[0].x, mz[1].x), fmaxf(mz[2].x, mz[3].x)));
+          const float zn = fmaxf(Z, fmaxf(fmaxf(mz[0].y, mz[1].y), fmaxf(mz[2].y, mz[3].y)));
+          const float f0 = exp2_fast(M - mn), mu = zn == -INFINITY ? 0.f : zn;
           M = mn;
-          L *= f0;
+          L *= exp2_fast(Z - mu);
+          Z = zn;
 #pragma unroll
           for (int e = 0; e < V; ++e) acc[e] *= f0;
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
-            const float f = exp2_fast(ml[p].x - mu);
-            L += ml[p].y * f;
+            const float f = exp2_fast(mz[p].x - mn);
+            L += exp2_fast(mz[p].y - mu);
 #pragma unroll
             for (int e = 0; e < V; ++e) acc[e] += v[p][e] * f;
           }
@@ -755,30 +769,38 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const AttnArgs a, const
   if constexpr (KW > 1) {
 #pragma unroll
     for (int e = 0; e < V; ++e) s_acc[half][k][V * lane + e] = acc[e];
-    if (lane == 0) s_ml[half][k] = make_float2(M, L);
+    if (lane == 0) {
+      s_mz[half][k] = make_float2(M, Z);
+      s_l[half][k] = L;
+    }
     __syncthreads();
-    M = -INFINITY;
+    M = kNothing;
+    Z = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < KW; ++w) M = fmaxf(M, s_ml[half][w].x);
-    const float mu = M == -INFINITY ? 0.f : M;
+    for (int w = 0; w < KW; ++w) {
+      M = fmaxf(M, s_mz[half][w].x);
+      Z = fmaxf(Z, s_mz[half][w].y);
+    }
+    const float mu = Z == -INFINITY ? 0.f : Z;
     L = 0.f;
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e] = 0.f;
 #pragma unroll
     for (int w = 0; w < KW; ++w) {
-      const float f = exp2_fast(s_ml[half][w].x - mu);
-      L += s_ml[half][w].y * f;
+      const float f = exp2_fast(s_mz[half][w].x - M);
+      L += s_l[half][w] * exp2_fast(s_mz[half][w].y - mu);
 #pragma unroll
       for (int e = 0; e < V; ++e) acc[e] += s_acc[half][w][V * lane + e] * f;
     }
   }
   if (!mine || k != 0) return;
-  const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+  Z = Z == -INFINITY ? 0.f : Z;
+  const float root = exp2_fast(0.5f * (M - Z)), inv = root * over(L);
 #pragma unroll
   for (int e = 0; e < V; e += 2)
-    *reinterpret_cast<uint32_t*>(a.O + row * D + V * lane + e) =
-        (uint32_t)float_to_bf16_bits(acc[e] * inv) | ((uint32_t)float_to_bf16_bits(acc[e + 1] * inv) << 16);
-  if (a.lse && lane == 0) a.lse[row] = L > 0.f || L != L ? M * kLn2 + logf(L) : -INFINITY;
+    *reinterpret_cast<uint32_t*>(a.O + row * D + V * lane + e) = (uint32_t)float_to_bf16_bits(acc[e] * inv * root) |
+                                                                 ((uint32_t)float_to_bf16_bits(acc[e + 1] * inv * root) << 16);
+  if (a.lse && lane == 0) a.lse[row] = L == 0.f ? -INFINITY : Z * kLn2 + logf(L);
 }
 
 }  // namespace kv

@@ -11,10 +11,10 @@
 //     step (of which two are held), then O += P V with P as the A operand from TMEM;
 //   * warps 0..3 and 4..7 (a thread for each of 128 rows, twice) turn S into P in place. While one half's
 //     softmax runs, the tensor cores work for the other half: S, P and O of both fill the 512 TMEM columns.
-// A row's reference maximum is raised only when the running one has outgrown it by 2^8, and the values' reference
-// scale only when a block's scale is 16 times it, so the outputs in TMEM are rarely rescaled; probabilities
-// relative to such a reference stay below 2^12 and are rounded to fp16. A block's value scale enters as an addend of
-// the exponent (log2(s / reference)), which costs nothing; sums are fp32.
+// A block's value scale s enters as an addend of the exponent, log2(s), which costs nothing: P holds weights p s, relative to
+// a reference of their own row. It is raised only when the running maximum has outgrown it by 2^8, so the outputs in
+// TMEM are rarely rescaled; weights stay below 2^8 and are rounded to fp16. The sum of the p is fp32, relative to a
+// reference of the scores alone: each group's weights times 1 / s. Nothing that a row does not see has a part in its result.
 // Measured: 2048-row chunks of four requests over up to 8192 keys, 32 query heads on 8 of 128: 710 us, 896 TFLOP/s (54 % of
 // the burst cuBLAS rate, 64 % of the sustained one, at 990 W); one prompt of 2048, 32 heads of their own: 67 us, of which
 // 9 us for each 256-row item are its beginning and end. A step of 64 keys takes 2280 cycles, of which the tensor cores work
@@ -37,16 +37,15 @@ constexpr int kPreGroups = kPreKeys / 16;
 constexpr int kPreStepGroups = kPreStep / 16;
 constexpr int kPreRing = 4;              // tiles whose scales are held
 constexpr float kPreLag = 8.f;           // log2 of how far the running maximum may outgrow its reference
-constexpr float kPreSlack = 16.f;        // the same for the values' reference scale
-constexpr float kPreLeast = -60.f;       // log2 of the smallest scale, relative to the reference, that is told apart
+constexpr int kPreApart = 8;             // the first step's bit, of a tile's: a scale so far below the largest (see kSpread)
 
 template <int D> struct __align__(1024) PreSmem {
   static constexpr int kPanels = D / 64;
   uint8_t q[2][kPanels][128 * 128];
   uint8_t k[2][kPanels][kPreKeys * 128];
   uint8_t v[2][kPanels][kPreKeys * 128];
-  // of each tile: [0, 8) key scales of the 16-key groups, [8, 16) log2 of their value scales relative to the
-  // reference, [16, 24) the inverses of those, [24] the reference, [25] bits of the groups that are not in the cache
+  // of each tile: [0, 8) key scales of the 16-key groups, [8, 16) log2 of their value scales, [16, 24) the inverses of
+  // those, [24] bits: the groups that are not in the cache, and from kPreApart the two steps
   float scale[kPreRing][32];
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2], p_full[2][2], o_full[2], o_last[2];
   uint64_t drained[2];
@@ -337,7 +336,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     const uint32_t s_addr = lane_base + (uint32_t)(128 * w), o_addr = lane_base + (uint32_t)(256 + 128 * w);
     // keys that every row of this warp sees, for the tiles that need no mask
     const int lane_lo = __reduce_max_sync(0xffffffffu, first), lane_hi = __reduce_min_sync(0xffffffffu, last);
-    float m = -INFINITY, l = 0.f, vref = 0.f;
+    float m = kNothing, ref = kNothing, l = 0.f;             // weights' reference, scores', and the sum relative to that
     bool ok = true;
     const int steps = 2 * (half[w].hi - half[w].lo);
     for (int n = 0; n < steps; ++n) {
@@ -350,16 +349,22 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       HBL_TMEM_LD32(src, x);
       HBL_TMEM_LD32(src + 32u, (x + 32));
       const uint32_t sc = tc::su32(&S.scale[(j - lo) % kPreRing][0]) + 16u * (n & 1);
-      const uint4 kq = lds128(sc), vq = lds128(sc + 32), iq = lds128(sc + 64);
-      const uint32_t sc0 = tc::su32(&S.scale[(j - lo) % kPreRing][0]);
-      const float vnow = lds32f(sc0 + 96);
-      const uint32_t bad = (__float_as_uint(lds32f(sc0 + 100)) >> (kPreStepGroups * (n & 1))) & 15u;
+      const uint4 kq = lds128(sc), vq = lds128(sc + 32);
+      const uint32_t bits = __float_as_uint(S.scale[(j - lo) % kPreRing][24]);
+      const uint32_t bad = (bits >> (kPreStepGroups * (n & 1))) & 15u;
       // never zero, so that a masked score (minus infinity) stays one when it is multiplied
       const float least = 1.17549435e-38f;
       const float f[4] = {fmaxf(__uint_as_float(kq.x) * qs, least), fmaxf(__uint_as_float(kq.y) * qs, least),
                           fmaxf(__uint_as_float(kq.z) * qs, least), fmaxf(__uint_as_float(kq.w) * qs, least)};
-      const float add[4] = {__uint_as_float(vq.x), __uint_as_float(vq.y), __uint_as_float(vq.z), __uint_as_float(vq.w)};
-      const float back[4] = {__uint_as_float(iq.x), __uint_as_float(iq.y), __uint_as_float(iq.z), __uint_as_float(iq.w)};
+      // addends of the exponent, relative to the reference; see kSpread
+      float add[4];
+      auto addends = [&](const uint4& lv, float lowest) {
+        add[0] = fmaxf(__uint_as_float(lv.x) - m, lowest);
+        add[1] = fmaxf(__uint_as_float(lv.y) - m, lowest);
+        add[2] = fmaxf(__uint_as_float(lv.z) - m, lowest);
+        add[3] = fmaxf(__uint_as_float(lv.w) - m, lowest);
+      };
+      addends(vq, -INFINITY);
       tc::tc_wait_ld();
       if (!(key0 >= lane_lo && key0 + kPreStep <= lane_hi && bad == 0)) {
         const int c_lo = first - key0, c_hi = last - key0;      // the columns that this row sees
@@ -367,7 +372,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         for (int i = 0; i < kPreStep; ++i)
           if (i < c_lo || i >= c_hi || (bad >> (i >> 4)) & 1) x[i] = 0xff800000u;
       }
-      float mt = -INFINITY;
+      float mt = -INFINITY, z[kPreStepGroups];
 #pragma unroll
       for (int g = 0; g < kPreStepGroups; ++g) {
         float y[5];
@@ -375,33 +380,43 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         for (int i = 0; i < 5; ++i)
           y[i] = max3(__uint_as_float(x[16 * g + 3 * i]), __uint_as_float(x[16 * g + 3 * i + 1]),
                       __uint_as_float(x[16 * g + 3 * i + 2]));
-        const float z = fmaxf(max3(y[0], y[1], y[2]), max3(y[3], y[4], __uint_as_float(x[16 * g + 15])));
-        mt = fmaxf(mt, z * f[g]);
+        z[g] = fmaxf(max3(y[0], y[1], y[2]), max3(y[3], y[4], __uint_as_float(x[16 * g + 15])));
+        mt = fmaxf(mt, __fmaf_rn(z[g], f[g], add[g]));
       }
-      const float mn = mt > m + kPreLag ? mt : m;
-      const float alpha = mn == m ? 1.f : exp2_fast(m - mn);
-      const float shrink = vref == vnow ? 1.f : __fdividef(vref, vnow);
-      vref = vnow;
-      m = mn;
-      l *= alpha;
-      const float ao = alpha * shrink;
-      if (n > 0 && __any_sync(0xffffffffu, ao != 1.f)) {
-        // Once the products so far are complete. Those up to the last but one are (this step's scores were issued behind
-        // them), and the next one waits for this step, so the phase is either this one or just over.
-        ok = __all_sync(0xffffffffu, wait(&S.o_full[w], (uint32_t)(n - 1) & 1u, abort));
-        if (!ok) break;
-        tc::tc_fence_after();
+      if (__any_sync(0xffffffffu, mt > kPreLag) || (bits >> (kPreApart + (n & 1)) & 1)) {
+        const uint4 lv = lds128(sc + 32);
+        const float u[4] = {z[0] * f[0], z[1] * f[1], z[2] * f[2], z[3] * f[3]};
+        const float most = fmaxf(fmaxf(u[0] + __uint_as_float(lv.x), u[1] + __uint_as_float(lv.y)),
+                                 fmaxf(u[2] + __uint_as_float(lv.z), u[3] + __uint_as_float(lv.w)));
+        const float mn = mt > kPreLag ? fmaxf(m, most) : m, rn = fmaxf(ref, fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])));
+        const float ao = exp2_fast(m - mn);
+        l *= exp2_fast(ref - rn);
+        m = mn;
+        ref = rn;
+        addends(lv, -ref - kSpread);
+        if (n > 0 && __any_sync(0xffffffffu, ao != 1.f)) {
+          // Once the products so far are complete. Those up to the last but one are (this step's scores were issued behind
+          // them), and the next one waits for this step, so the phase is either this one or just over.
+          ok = __all_sync(0xffffffffu, wait(&S.o_full[w], (uint32_t)(n - 1) & 1u, abort));
+          if (!ok) break;
+          tc::tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t o[16];
-          HBL_TMEM_LD16(o_addr + 16u * c, o);
-          tc::tc_wait_ld();
+          for (int k = 0; k < D / 16; ++k) {
+            uint32_t o[16];
+            HBL_TMEM_LD16(o_addr + 16u * k, o);
+            tc::tc_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * ao);
-          HBL_TMEM_ST16(o_addr + 16u * c, o);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * ao);
+            HBL_TMEM_ST16(o_addr + 16u * k, o);
+          }
         }
       }
-      const float mu = m == -INFINITY ? 0.f : m;
+      // From weights to p: a block's 1 / s, and the references; 2^96 at most (see kSpread), also where this is infinity times
+      // zero, a row that has seen scales of 0 alone.
+      const float kappa = exp2_fast(m - ref), most_back = __uint_as_float((127u + (uint32_t)kSpread) << 23);
+      const uint4 iq = lds128(sc + 64);
+      const float back[4] = {fminf(__uint_as_float(iq.x) * kappa, most_back), fminf(__uint_as_float(iq.y) * kappa, most_back),
+                             fminf(__uint_as_float(iq.z) * kappa, most_back), fminf(__uint_as_float(iq.w) * kappa, most_back)};
       // A pair's exponentials take the special function unit 16 cycles; the arithmetic of the pair kLag in front is issued
       // in their shadow, in this order, and never waits for them.
       constexpr int kPairs = kPreStep / 2, kLag = 4;
@@ -410,7 +425,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
 #pragma unroll
       for (int i = 0; i < kPairs + kLag; ++i) {
         if (i < kPairs) {
-          const float ag = add[i >> 3] - mu;
+          const float ag = add[i >> 3];
           const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
                                       make_float2(f[i >> 3], f[i >> 3]), make_float2(ag, ag));
           x[2 * i] = __float_as_uint(exp2_ordered(y.x));
@@ -438,7 +453,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     if (ok && !*abort) {
       tc::tc_fence_after();
       const bool some = l > 0.f || l != l;
-      const float inv = some ? vref / l : 0.f;
+      const float inv = over(l) * exp2_fast(m - ref);
       const size_t out = (size_t)(rq.row0 + tok) * a.Hq + head;
       // Each lane has a row; through the place of the half's queries, whose last use is over, a warp's stores become whole
       // lines (two or four rows at a time).
@@ -474,7 +489,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         if (row < nrows)
           reinterpret_cast<uint4*>(a.O + ((size_t)(rq.row0 + t) * a.Hq + (size_t)(h * a.group + row - t * a.group)) * D)[c] = v;
       }
-      if (live && a.lse) a.lse[out] = some ? m * kLn2 + logf(l) : -INFINITY;
+      if (live && a.lse) a.lse[out] = some ? ref * kLn2 + logf(l) : -INFINITY;
     }
   } else if (warp < 12) {
     // ----- codes to fp16 -----
@@ -619,18 +634,19 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       }
     } else if (warp == 13) {
       // ----- block scales -----
-      // Lane g < 8 holds those of group g. The key scale of a group that no row sees is 1, whatever its page has.
+      // Lane g (mod 8) holds those of group g. The scales of a group that no row of the CTA sees are 1, whatever its page has.
       const int32_t* table = a.table + (size_t)b * a.max_pages;
       const int any_first = a.window > 0 ? max(rq.kv - rq.q + by_group(a, row0) + 1 - a.window, 0) : 0;
-      float ks = 1.f, vs = 0.f, vref = 0.f;
+      const int any_last = a.causal ? rq.kv - rq.q + by_group(a, min(row0 + kPreRows, nrows) - 1) + 1 : rq.kv;
+      float ks = 1.f, vs = 1.f, top = 0.f;                   // top: the largest value scale so far
       bool absent = false;
       PageLookup look;
       auto load = [&](int j) {
         look.settle(a);
-        ks = 1.f;
-        vs = 0.f;
+        const int key = j * kPreKeys + 16 * (lane & 7);
+        ks = vs = 1.f;
         absent = look.id == -1;
-        if (look.id >= 0 && j * kPreKeys + 16 * (lane & 7) + 16 > any_first) {
+        if (look.id >= 0 && key + 16 > any_first && key < any_last) {
           ks = __ldg(a.kscale + (size_t)look.id * a.Hkv + h);
           vs = __ldg(a.vscale + (size_t)look.id * a.Hkv + h);
         }
@@ -642,12 +658,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       }
       for (int j = lo; j < hi; ++j) {
         const int n = j - lo, st = n & 1;
-        float vm = vs;
-#pragma unroll
-        for (int o = 1; o < kPreGroups; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+        const float lv = log2_scale(vs);
         const unsigned bad = __ballot_sync(0xffffffffu, absent) & 0xffu;
-        if (vref == 0.f || vm > kPreSlack * vref) vref = vm;
-        const float lv = vs > 0.f ? fmaxf(__log2f(__fdividef(vs, vref)), kPreLeast) : kPreLeast;
+        top = fmaxf(top, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vs))));    // scales are not negative
+        const unsigned apart = __ballot_sync(0xffffffffu, lv < fmaxf(log2_scale(top), kLeastScale) - kSpread);
         // the ring's place is free: k_full of tile n - 1 was signalled behind the scores of tile n - 3, which wait for
         // the probabilities of tile n - 4, its last user
         if (lane < kPreGroups) {
@@ -656,8 +670,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
           dst[8 + lane] = lv;
           dst[16 + lane] = exp2_fast(-lv);
           if (lane == 0) {
-            dst[24] = vref;
-            dst[25] = __uint_as_float(bad);
+            dst[24] = __uint_as_float(bad | (apart & 0x0fu ? 1u << kPreApart : 0u) | (apart & 0xf0u ? 2u << kPreApart : 0u));
             if (bad) set_device_error(HBL_ERR_INVALID_ARG);
           }
         }

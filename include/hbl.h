@@ -367,11 +367,13 @@ size_t hbl_kv_attention_workspace_bytes(int B, int D);
  *   ws      : device workspace, 256-byte aligned, clobbered; calls whose
  *             execution overlaps must not share it.
  * A row that sees no key gives zeros and an lse of -infinity. A key whose
- * page is not in the cache counts as absent. Masked keys have no influence,
- * whatever they hold. Scales must be finite and not negative. Scores, sums and
- * outputs are fp32; probabilities are rounded to fp16 relative to the largest
- * of a row's value scales (an absolute error of at most 2^-25 for each key where they
- * are small). T * Hq < 2^30.
+ * page is not in the cache counts as absent. Keys that a row does not see have
+ * no influence on it; pages that no row sees may hold anything. Scales of the
+ * others must be finite and not negative. Scores, sums and outputs are fp32. A
+ * key's weight, its probability times its value scale, is rounded to fp16
+ * relative to the largest weight of the row: by 2^-11 of itself, or by 2^-25 of
+ * the largest where that is more. Value scales below 2^-118, but for 0, count as
+ * that much. T * Hq < 2^30.
  */
 int hbl_kv_attention(const hbl_bf16* Q, int T, int Hq, int Hkv, int D, long long q_stride,
                      const int32_t* cu_q, const int32_t* kv_lens, int B, int max_q, int max_kv,

@@ -726,3 +726,147 @@ def test_attention_few_rows_beyond_the_bound_are_left(L, q, kv, kw, many):
     want = reference(cache, Q, cu, kvs, table)
     want[1][left] = np.nan
     close(out, lse, want, float(cache.vscale.max()), 50)
+
+
+# ----------------------------------------------------------------------------- a row and the keys that it sees
+def own_bounds(case, scale=None, causal=True, window=0, lag=0):
+    """(out, lse, bound, lse bound) of each row from the keys that it sees alone, and nothing of other rows, heads or
+    requests; NaN where a row belongs to no request.
+
+    A weight is w = p s, of the key's probability and value scale. It is rounded to fp16 relative to a reference that is
+    never above 2^lag of the row's largest weight: by 2^-11 of itself, or by 2^-25 of the reference where that is more,
+    times a code of at most 127. Scales below 2^-118, but for 0, count as that much. delta is ``close``'s, but that the log2 of a scale is added to the exponent: up to 2^8,
+    off by 2^-17 once for the weight and once for the sum.
+    """
+    cache, Q, cu, kvs, table = case
+    Q, page, D = np64(Q), cache.page, cache.head_dim
+    scale = D ** -0.5 if scale is None else scale
+    codes = [c.cpu().numpy().astype(np.float64) - 128 for c in (cache.kcodes, cache.vcodes)]
+    ks, vs = (s.double().cpu().numpy() for s in (cache.kscale, cache.vscale))
+    T, heads, _ = Q.shape
+    out, bound = np.full((2, T, heads, D), np.nan)
+    lse, off = np.full((2, T, heads), np.nan)
+    for b, kv in enumerate(int(k) for k in kvs):
+        rows = np.arange(cu[b], cu[b + 1])
+        j = np.arange(kv)
+        pos = kv - len(rows) + np.arange(len(rows))[:, None]
+        seen = np.ones((len(rows), kv), bool) if not causal else j <= pos
+        if window:
+            seen = seen & (j > pos - window)
+        at, o = table[b, j // page], j % page
+        for i in range(heads):
+            h = i // (heads // cache.kv_heads)
+            k, v, s = codes[0][at, h, o] * ks[at, h][:, None], codes[1][at, h, o], vs[at, h]
+            a = np.where(seen, scale * (Q[rows, i] @ k.T), -np.inf)
+            spread = scale * np.max(np.where(seen, np.abs(Q[rows, i]) @ np.abs(k).T, 0), axis=1, initial=0)
+            m = np.max(a, axis=1, initial=-np.inf, keepdims=True)
+            p = np.exp(a - np.where(np.isneginf(m), 0, m))
+            l = p.sum(1)
+            w = p * s
+            delta = spread * (D + 6) * 2.0 ** -23 + 2.0 ** -20 + 2.0 ** -16
+            with np.errstate(divide="ignore", invalid="ignore"):
+                lse[rows, i] = m[:, 0] + np.log(l)
+                inv = np.where(l > 0, 1 / l, 0)
+            out[rows, i] = (w @ v) * inv[:, None]
+            mag = (w @ np.abs(v)) * inv[:, None]
+            tiny = 2.0 ** (lag - 25) * 127 * w.max(1, initial=0) * inv * seen.sum(1)
+            bound[rows, i] = 2.0 ** -8 * np.abs(out[rows, i]) + (2.0 ** -11 + 4 * delta[:, None]) * mag + tiny[:, None]
+            off[rows, i] = delta + np.abs(np.where(l > 0, lse[rows, i], 0)) * 2.0 ** -21
+    return out, lse, bound, off
+
+
+def check_rows(case, **kw):
+    cache, Q, cu, kvs, table = case
+    out, lse, bound, off = own_bounds(case, **kw)
+    kw.pop("lag", None)
+    got, glse = (np64(x) for x in cache.attention(Q, i32(cu), i32(kvs), i32(table), return_lse=True, **kw))
+    rows = ~np.isnan(lse)
+    some = rows & np.isfinite(lse)
+    assert np.array_equal(np.isneginf(glse[rows]), np.isneginf(lse[rows]))
+    assert np.all(np.abs(glse - lse)[some] <= off[some]), float(np.max((np.abs(glse - lse) - off)[some]))
+    worst = np.abs(got - out) - bound
+    assert np.all(worst[rows] <= 0), (float(np.max(worst[rows])), np.argwhere(rows)[np.argmax(worst.max(2)[rows])])
+
+
+# rows of a request, query heads, key/value heads: 8 rows a tile, 16 rows, and more, which `many` sends to the tensor cores
+SHAPES = pytest.mark.parametrize("q,Hq,Hkv,D,page,many", [
+    (6, 2, 2, 128, 16, False), (6, 2, 2, 64, 16, False), (20, 2, 2, 128, 16, False), (15, 4, 2, 64, 32, False),
+    (60, 2, 1, 128, 16, True), (300, 2, 2, 64, 16, True), (150, 4, 1, 128, 64, True)])
+
+
+@SHAPES
+@pytest.mark.parametrize("louder", [14, 20, 28, 40, 110])
+def test_attention_later_keys_do_not_round_a_row(L, q, Hq, Hkv, D, page, many, louder):
+    """Values that only later rows see are louder by far; a row's result is as exact as without them."""
+    for kv in (q, q + 2 * page + 3):
+        case = make_case(L, 24, [q, 3], [kv, 2 * page], Hq, Hkv, D, page, spare(many, Hq))
+        cache, _, _, _, table = case
+        first = max(kv - q // 2, page) // page               # pages from here on are loud
+        at = torch.tensor(table[0, first:-(-kv // page)], device="cuda").long()
+        cache.vscale[at] *= 2.0 ** louder
+        check_rows(case)
+
+
+@SHAPES
+@pytest.mark.parametrize("louder", [20, 40])
+def test_attention_keys_before_the_window_do_not_round_a_row(L, q, Hq, Hkv, D, page, many, louder):
+    """Loud values in front of a row's window, which earlier rows see."""
+    kv = q + 4 * page + 5
+    case = make_case(L, 25, [q], [kv], Hq, Hkv, D, page, spare(many, Hq))
+    cache, _, _, _, table = case
+    window = 5
+    last = (kv - q + 1) // page                              # the first rows' keys and all before them
+    cache.vscale[torch.tensor(table[0, :last + 1], device="cuda").long()] *= 2.0 ** louder
+    check_rows(case, window=window)
+
+
+@SHAPES
+def test_attention_largest_and_smallest_values_side_by_side(L, q, Hq, Hkv, D, page, many):
+    """What appending makes of an infinity, of zeros and of ordinary values, over all that a row sees: the largest stay
+    finite, and the smallest count in the sum."""
+    kv = max(q, 12 * page)
+    case = make_case(L, 26, [q], [kv], Hq, Hkv, D, page, spare(many, Hq))
+    cache, Q, cu, kvs, table = case
+    top = float(torch.tensor((2 - 2 ** -7) * 2.0 ** 127 / 127, dtype=torch.float32))
+    pages = torch.tensor(table[0, :-(-kv // page)], device="cuda").long()
+    for scales in ((top,), (2.0 ** -100,), (top, 2.0 ** -100), (2.0 ** -100, 0.01), (2.0 ** -100, 0.01, top, 0.3), (0.0, top),
+                   (0.0, 2.0 ** -100), (0.0,), (2.0 ** 20, 2.0 ** -100, 2.0 ** -60)):
+        for n, p in enumerate(pages):
+            cache.vscale[p] = scales[n % len(scales)]
+        check_rows(case)
+    cache.vscale[pages] = top
+    cache.vcodes[pages] = 255
+    check_rows(case)
+    out = cache.attention(Q, i32(cu), i32(kvs), i32(table))[:q]
+    assert out.isfinite().all()
+
+
+@BOTH
+def test_attention_masked_pages_of_prompts_have_no_influence(L, many):
+    """NaN and infinite scales of pages that no row of the request sees."""
+    case = make_case(L, 27, [80], [400], 4, 2, 128, 16, spare(many, 4))
+    cache, Q, cu, kvs, table = case
+    args = i32(cu), i32(kvs), i32(table)
+    want = [x[:80].clone() for x in cache.attention(Q, *args, window=50, return_lse=True)]
+    used = {int(table[0, j]) for j in range((400 - 80 + 1 - 50) // 16, 25)}
+    for p in range(cache.num_pages):
+        if p not in used:
+            cache.kscale[p], cache.vscale[p] = float("nan"), float("inf")
+    again = cache.attention(Q, *args, window=50, return_lse=True)
+    assert torch.equal(want[0], again[0][:80]) and torch.equal(want[1], again[1][:80])
+
+
+@SHAPES
+@pytest.mark.parametrize("seed", [0, 1, 2])
+def test_attention_scores_against_value_scales(L, q, Hq, Hkv, D, page, many, seed):
+    """Scores about a hundred powers of two apart and value scales as far: the keys with the largest weights are not those
+    with the largest probabilities."""
+    kv = max(q, 9 * page + 5)
+    case = make_case(L, 28 + seed, [q, 1], [kv, 5 * page], Hq, Hkv, D, page, spare(many, Hq))
+    cache = case[0]
+    rng = np.random.default_rng(seed)
+    cache.kscale.copy_(torch.tensor(2.0 ** rng.uniform(-6, 0, cache.kscale.shape), dtype=torch.float32))
+    cache.vscale.copy_(torch.tensor(2.0 ** rng.uniform(-100, 110, cache.vscale.shape), dtype=torch.float32))
+    check_rows(case)
+    check_rows(case, causal=False)
+    check_rows(case, window=3 * page)
