@@ -19,7 +19,7 @@
 //     the second product takes weights p s, relative to a reference of their own row: nothing that a row does not see
 //     has a part in how they are rounded. The sum of the p, relative to a reference of the scores alone, is that of the
 //     weights times 1 / s. Both references are raised only when a tile outgrows the weights' by 2^8: then no lane has to ask
-//     the others for the tile's maxima. Weights stay below 2^8 and are rounded to fp16 (11 bits), finer than the bf16 output.
+//     the others for the tile's maxima. Weights stay below 2^15 and are rounded to fp16 (11 bits), finer than the bf16 output.
 // At the end of a run the warps' results are joined through shared memory: weighted values relative to the largest weights'
 // reference, and the log2 of the sums. A run that is only a part of its row's keys goes to the workspace in the same form,
 // and kv_combine_kernel joins the parts.
@@ -37,13 +37,15 @@ namespace kv {
 
 constexpr int kAttnTile = 32;         // tokens of a warp's tile
 constexpr int kAttnRows = 16;         // most query rows of a tile
-constexpr float kLag = 8.f;           // log2 of how far a tile may outgrow the reference
+// log2 of how far the weights' reference is set below the largest weight, and of how far that may then grow: together fp16's
+// range, so that small weights, of which there may be many, are rounded as late as its least value allows.
+constexpr float kHead = 7.f, kLag = 8.f;
 // log2 of how far a block's value scale may lie below that of the row's largest weight before the scores' reference is brought
-// up to date (the sum, relative to it, stays below 2^104 for each key). With one that lies further below the block then counts
+// up to date (the sum, relative to it, stays below 2^103 for each key). With one that lies further below the block then counts
 // as that far: its weights are zero in fp16 either way, and the p that the sum gets back from them neither vanish nor
 // overflow. kLeastScale: log2 of the least value scale that is told apart (appending makes none below 2^-100); kZeroScale
 // stands for that of 0, which leaves the weights' reference as it is.
-constexpr float kSpread = 96.f, kLeastScale = -118.f, kZeroScale = -2e30f;
+constexpr float kSpread = 88.f, kLeastScale = -110.f, kZeroScale = -2e30f;
 constexpr float kNothing = -1e30f;    // references of a row that has seen no key
 constexpr int kMaxAttnCtas = 480;     // workspace is laid out for this many
 constexpr float kLog2e = 1.4426950408889634f;
@@ -523,7 +525,7 @@ __global__ void __launch_bounds__(AttnCfg<D>::kWarps * 32, AttnCfg<D>::kCtas) kv
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float s0 = fmaxf(s[i][0][e], s[i][0][e + 2]), s1 = fmaxf(s[i][1][e], s[i][1][e + 2]);
-            grown |= fmaxf(s0 + lv[0], s1 + lv[1]) > m[i][e] + kLag || quiet < m[i][e] - ref[i][e] - kSpread;
+            grown |= fmaxf(s0 + lv[0], s1 + lv[1]) > m[i][e] + (kHead + kLag) || quiet < m[i][e] - ref[i][e] - kSpread;
           }
         if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
@@ -537,7 +539,7 @@ __global__ void __launch_bounds__(AttnCfg<D>::kWarps * 32, AttnCfg<D>::kCtas) kv
                 y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
                 ys = fmaxf(ys, __shfl_xor_sync(0xffffffffu, ys, d));
               }
-              const float mn = fmaxf(m[i][e], y), rn = fmaxf(ref[i][e], ys);
+              const float mn = fmaxf(m[i][e], y - kHead), rn = fmaxf(ref[i][e], ys);
               const float alpha = exp2_fast(m[i][e] - mn);
               l[i][e] *= exp2_fast(ref[i][e] - rn);
               m[i][e] = mn;

@@ -12,8 +12,8 @@
 //   * warps 0..3 and 4..7 (a thread for each of 128 rows, twice) turn S into P in place. While one half's
 //     softmax runs, the tensor cores work for the other half: S, P and O of both fill the 512 TMEM columns.
 // A block's value scale s enters as an addend of the exponent, log2(s), which costs nothing: P holds weights p s, relative to
-// a reference of their own row. It is raised only when the running maximum has outgrown it by 2^8, so the outputs in
-// TMEM are rarely rescaled; weights stay below 2^8 and are rounded to fp16. The sum of the p is fp32, relative to a
+// a reference of their own row, 2^7 below the largest. It is raised only when that has grown by 2^8, so the outputs in
+// TMEM are rarely rescaled; weights stay below 2^15 and are rounded to fp16. The sum of the p is fp32, relative to a
 // reference of the scores alone: each group's weights times 1 / s. Nothing that a row does not see has a part in its result.
 // Measured: 2048-row chunks of four requests over up to 8192 keys, 32 query heads on 8 of 128: 710 us, 896 TFLOP/s (54 % of
 // the burst cuBLAS rate, 64 % of the sustained one, at 990 W); one prompt of 2048, 32 heads of their own: 67 us, of which
@@ -36,7 +36,6 @@ constexpr int kPreThreads = 512;
 constexpr int kPreGroups = kPreKeys / 16;
 constexpr int kPreStepGroups = kPreStep / 16;
 constexpr int kPreRing = 4;              // tiles whose scales are held
-constexpr float kPreLag = 8.f;           // log2 of how far the running maximum may outgrow its reference
 constexpr int kPreApart = 8;             // the first step's bit, of a tile's: a scale so far below the largest (see kSpread)
 
 template <int D> struct __align__(1024) PreSmem {
@@ -383,12 +382,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         z[g] = fmaxf(max3(y[0], y[1], y[2]), max3(y[3], y[4], __uint_as_float(x[16 * g + 15])));
         mt = fmaxf(mt, __fmaf_rn(z[g], f[g], add[g]));
       }
-      if (__any_sync(0xffffffffu, mt > kPreLag) || (bits >> (kPreApart + (n & 1)) & 1)) {
+      if (__any_sync(0xffffffffu, mt > kHead + kLag) || (bits >> (kPreApart + (n & 1)) & 1)) {
         const uint4 lv = lds128(sc + 32);
         const float u[4] = {z[0] * f[0], z[1] * f[1], z[2] * f[2], z[3] * f[3]};
         const float most = fmaxf(fmaxf(u[0] + __uint_as_float(lv.x), u[1] + __uint_as_float(lv.y)),
                                  fmaxf(u[2] + __uint_as_float(lv.z), u[3] + __uint_as_float(lv.w)));
-        const float mn = mt > kPreLag ? fmaxf(m, most) : m, rn = fmaxf(ref, fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])));
+        const float mn = mt > kHead + kLag ? fmaxf(m, most - kHead) : m, rn = fmaxf(ref, fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])));
         const float ao = exp2_fast(m - mn);
         l *= exp2_fast(ref - rn);
         m = mn;
@@ -411,7 +410,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
           }
         }
       }
-      // From weights to p: a block's 1 / s, and the references; 2^96 at most (see kSpread), also where this is infinity times
+      // From weights to p: a block's 1 / s, and the references; 2^88 at most (see kSpread), also where this is infinity times
       // zero, a row that has seen scales of 0 alone.
       const float kappa = exp2_fast(m - ref), most_back = __uint_as_float((127u + (uint32_t)kSpread) << 23);
       const uint4 iq = lds128(sc + 64);

@@ -371,8 +371,8 @@ size_t hbl_kv_attention_workspace_bytes(int B, int D);
  * no influence on it; pages that no row sees may hold anything. Scales of the
  * others must be finite and not negative. Scores, sums and outputs are fp32. A
  * key's weight, its probability times its value scale, is rounded to fp16
- * relative to the largest weight of the row: by 2^-11 of itself, or by 2^-25 of
- * the largest where that is more. Value scales below 2^-118, but for 0, count as
+ * relative to the largest weight of the row: by 2^-11 of itself, or by 2^-32 of
+ * the largest where that is more. Value scales below 2^-110, but for 0, count as
  * that much. T * Hq < 2^30.
  */
 int hbl_kv_attention(const hbl_bf16* Q, int T, int Hq, int Hkv, int D, long long q_stride,

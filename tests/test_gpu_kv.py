@@ -735,7 +735,7 @@ def own_bounds(case, scale=None, causal=True, window=0, lag=0):
 
     A weight is w = p s, of the key's probability and value scale. It is rounded to fp16 relative to a reference that is
     never above 2^lag of the row's largest weight: by 2^-11 of itself, or by 2^-25 of the reference where that is more,
-    times a code of at most 127. Scales below 2^-118, but for 0, count as that much. delta is ``close``'s, but that the log2 of a scale is added to the exponent: up to 2^8,
+    times a code of at most 127. Scales below 2^-110, but for 0, count as that much. delta is ``close``'s, but that the log2 of a scale is added to the exponent: up to 2^8,
     off by 2^-17 once for the weight and once for the sum.
     """
     cache, Q, cu, kvs, table = case
@@ -870,3 +870,24 @@ def test_attention_scores_against_value_scales(L, q, Hq, Hkv, D, page, many, see
     check_rows(case)
     check_rows(case, causal=False)
     check_rows(case, window=3 * page)
+
+
+@pytest.mark.parametrize("q,Hq,Hkv,D,page,many", [(1, 2, 2, 128, 16, False), (1, 8, 1, 64, 64, False), (12, 2, 1, 128, 32, False),
+                                                  (40, 2, 1, 128, 16, True), (300, 1, 1, 64, 32, True)])
+@pytest.mark.parametrize("below", [24.0, 25.2, 27.3])
+def test_attention_many_keys_of_small_weight(L, q, Hq, Hkv, D, page, many, below):
+    """One key that takes nearly all of the probability and has no value, beside thousands 2^-25 as probable: they are
+    the whole output, and rounded relative to 2^-7 of the largest weight."""
+    kv = 20000 if q == 1 else 3000
+    case = make_case(L, 31, [q], [kv], Hq, Hkv, D, page, spare(many, Hq))
+    cache, Q, cu, kvs, table = case
+    Q.fill_(1.0)
+    cache.kcodes.fill_(128)
+    cache.vcodes.copy_(cache.vcodes.clamp(min=150))
+    cache.vscale.fill_(0.25)
+    cache.kscale.fill_(below * np.log(2) / (D ** 0.5 * 100))
+    first = int(table[0, 1])                                 # not the first key: the reference is raised on the way
+    cache.kcodes[first, :, 3] = 228
+    cache.vcodes[first, :, 3] = 128
+    check_rows(case, lag=-7)
+    check_rows(case, lag=-7, causal=False)
