@@ -213,7 +213,7 @@ int hbl_kv_attention(const hbl_bf16* Q, int T, int Hq, int Hkv, int D, long long
   if ((long long)T * Hq >= (1ll << 30) || (st = check_table(B, max_pages, page))) return HBL_ERR_SHAPE;
   if (max_q < 0 || max_kv < 0) return HBL_ERR_SHAPE;
   if ((causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal)) return HBL_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return HBL_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale * kv::kLog2e)) return HBL_ERR_INVALID_ARG;
   if (T == 0 || B == 0) return HBL_OK;
   if (!Q || !cu_q || !kv_lens || !block_table || !kcodes || !vcodes || !kscale || !vscale || !O)
     return HBL_ERR_INVALID_ARG;

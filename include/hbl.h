@@ -358,7 +358,7 @@ size_t hbl_kv_attention_workspace_bytes(int B, int D);
  *   max_kv  : the most cached tokens likewise (0: max_pages * page). A hint by
  *             which kernels are chosen; with a wrong one the rows are right,
  *             only slower.
- *   scale   : finite, > 0; multiplies the scores.
+ *   scale   : > 0, at most 2^127; multiplies the scores.
  *   causal  : 1: row i of q sees the keys up to position kv - q + i; 0: all.
  *   window  : > 0 (with causal only): and of those the last `window`. 0: none.
  *   O       : device bf16 T x Hq x D, written for the rows of the requests; rows

@@ -135,3 +135,27 @@ def test_noalloc_rejects_sizes_beyond_its_array(lib):
     assert hbl.hbl_workspace_bytes(16, 4096, 4096) <= 8 << 20
     # still refused on its arguments first
     assert lib.hbl_forward_noalloc(BAD, 4096, 16384, 256, BAD, BAD, 5, 1, BAD, None) == 1
+
+
+def kv_attention_args(**kw):
+    """Arguments of a call that would be launched, some of them changed."""
+    a = dict(Q=BAD, T=4, Hq=8, Hkv=2, D=128, q_stride=1024, cu_q=BAD, kv_lens=BAD, B=2, max_q=0, max_kv=0, block_table=BAD,
+             max_pages=8, page=16, num_pages=20, kcodes=BAD, vcodes=BAD, kscale=BAD, vscale=BAD, scale=0.1, causal=1, window=0,
+             O=BAD, lse=None, ws=BAD, ws_bytes=1 << 30, stream=None)
+    assert set(kw) <= set(a)
+    return list({**a, **kw}.values())
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1),
+    (dict(scale=3e38), 1),                       # times log2(e) no longer a float
+    (dict(causal=2), 1), (dict(window=-1), 1), (dict(causal=0, window=4), 1),
+    (dict(page=20), 2), (dict(page=256), 2), (dict(num_pages=0), 2), (dict(num_pages=1 << 27), 2), (dict(D=96), 2),
+    (dict(T=-1), 2), (dict(T=1 << 27), 2), (dict(Hq=7), 2), (dict(q_stride=1016), 2), (dict(q_stride=1028), 2),
+    (dict(B=-1), 2), (dict(B=8193), 2), (dict(max_pages=0), 2), (dict(max_pages=1 << 28), 2), (dict(max_q=-1), 2),
+    (dict(max_kv=-1), 2), (dict(Q=None), 1), (dict(O=None), 1), (dict(vscale=None), 1), (dict(Q=BAD + 2), 1),
+    (dict(lse=BAD + 2), 1), (dict(ws=None), 7), (dict(ws_bytes=1000), 7), (dict(ws=BAD + 16), 1),
+    (dict(T=0, Q=None, O=None), 0), (dict(B=0, cu_q=None), 0),
+])
+def test_kv_attention_argument_checks(lib, kw, status):
+    assert lib.hbl_kv_attention(*kv_attention_args(**kw)) == status
