@@ -225,7 +225,7 @@ class KVCache:
             assert lse.shape == (T, Hq) and lse.dtype is torch.float32 and lse.is_contiguous()
             assert lse.get_device() == Q.get_device()
         if ws is not None:
-            assert ws.dtype is torch.uint8 and ws.get_device() == Q.get_device()
+            assert ws.dtype is torch.uint8 and ws.is_contiguous() and ws.get_device() == Q.get_device()
         with _allocating(stream):
             if out is None:
                 out = Q.new_empty(T, Hq, D)

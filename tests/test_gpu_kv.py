@@ -891,3 +891,14 @@ def test_attention_many_keys_of_small_weight(L, q, Hq, Hkv, D, page, many, below
     cache.vcodes[first, :, 3] = 128
     check_rows(case, lag=-7)
     check_rows(case, lag=-7, causal=False)
+
+
+def test_a_workspace_is_whole(L):
+    """A strided view has bytes between its own that are not the call's to write."""
+    case = make_case(L, 32, [1, 1], [40, 30], 4, 2, 64, 16)
+    cache, Q, cu, kvs, table = case
+    need = cache.workspace(2).numel()
+    wide = torch.zeros(need, 2, dtype=torch.uint8, device="cuda")
+    with pytest.raises(AssertionError):
+        cache.attention(Q, i32(cu), i32(kvs), i32(table), ws=wide[:, 0])
+    assert bool((wide == 0).all())
