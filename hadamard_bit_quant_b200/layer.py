@@ -219,6 +219,7 @@ class KVCache:
         T, Hq, D = Q.shape
         B, max_pages = block_table.shape
         assert kv_lens.numel() == B and cu_q.numel() == B + 1 and kv_lens.get_device() == self.kcodes.get_device()
+        assert max(max_q, max_kv, window) < 1 << 31 and min(max_q, max_kv, window) >= -1 << 31     # ctypes would cut them
         if out is not None:
             assert out.shape == Q.shape and out.is_contiguous() and self._rows(out) == Hq * D
         if lse is not None:

@@ -902,3 +902,12 @@ def test_a_workspace_is_whole(L):
     with pytest.raises(AssertionError):
         cache.attention(Q, i32(cu), i32(kvs), i32(table), ws=wide[:, 0])
     assert bool((wide == 0).all())
+
+
+@pytest.mark.parametrize("kw", [{"max_q": 2 ** 32 + 1}, {"max_kv": 2 ** 31}, {"window": 2 ** 32 + 3}, {"window": 3 - 2 ** 32}])
+def test_numbers_wider_than_an_int_are_refused(L, kw):
+    """Cut to 32 bits they would be other numbers: a window of 3, a bound of one row."""
+    case = make_case(L, 33, [5, 1], [40, 30], 4, 2, 64, 16)
+    cache, Q, cu, kvs, table = case
+    with pytest.raises(AssertionError):
+        cache.attention(Q, i32(cu), i32(kvs), i32(table), **kw)
