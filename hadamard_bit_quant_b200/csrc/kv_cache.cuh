@@ -272,7 +272,7 @@ HBL_DEVINL void append_run(const uint16_t* x, long long stride, int n, int off, 
   constexpr int VPT = D / 8;          // vectors of a token
   const int total = n * VPT;
   const float held = off > 0 ? *scale : 0.f;
-  const float before = held >= 0.f && held <= 3.4e38f ? held : 0.f;
+  const float before = held >= 0.f && held < INFINITY ? held : 0.f;
   auto vec = [&](int i) { return __ldg(reinterpret_cast<const uint4*>(x + (size_t)(i / VPT) * (size_t)stride) + i % VPT); };
   uint4 v[HELD];
   uint32_t m = 0;

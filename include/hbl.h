@@ -320,7 +320,8 @@ int hbl_kv_plan(const int32_t* new_lens, int B, int page, int num_pages, int max
  *   slots  : device int32 T; a negative slot is skipped.
  * Tokens in consecutive slots of one page form a run. With gamma the run's
  * absmax in a head, the block's scale becomes
- *   s = max(s_before, gamma / 127, 2^-100)   (s_before = 0 if the run begins the page),
+ *   s = max(s_before, gamma / 127, 2^-100)   (s_before = 0 if the run begins the page, or
+ * where the block's scale is negative or not finite),
  * codes that the block held before the run become rint(c * s_before / s), the
  * new ones rint(x / s) (exact quotients, ties to even). NaN is stored as 0, an
  * infinity as the largest finite value. Tokens that a page held behind the

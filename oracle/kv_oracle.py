@@ -73,7 +73,7 @@ def kv_append(x, slots, codes, scale, page):
             gamma = np.max(np.abs(x[t:end, h]))
             before = scale[p, h] if off else np.float32(0)
             s = max(before, np.float32(gamma / 127.0), np.float32(KV_SCALE_FLOOR))
-            for j in range(off):
+            for j in range(off if s != before else 0):       # c * s / s is c, also where c * s is no float
                 held = np.float32((codes[p, h, j].astype(np.float64) - 128.0) * np.float64(before))
                 codes[p, h, j] = (np.rint(held.astype(np.float64) / np.float64(s)) + 128).astype(np.uint8)
             codes[p, h, off:off + end - t] = (np.rint(x[t:end, h] / np.float64(s)) + 128).astype(np.uint8)

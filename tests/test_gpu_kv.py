@@ -911,3 +911,26 @@ def test_numbers_wider_than_an_int_are_refused(L, kw):
     cache, Q, cu, kvs, table = case
     with pytest.raises(AssertionError):
         cache.attention(Q, i32(cu), i32(kvs), i32(table), **kw)
+
+
+@pytest.mark.parametrize("H,D,page", [(2, 64, 16), (3, 128, 64)])
+def test_append_to_blocks_of_odd_scales(L, H, D, page):
+    """Scales that no append has left: of no matter where a run begins the page, and 0 elsewhere if negative or not finite."""
+    rng = np.random.default_rng(41)
+    odd = [np.nan, np.inf, -np.inf, -1.0, -0.0, 3.4025e38, 1e-45, 2.0 ** -110, 1e30]
+    runs = [(p, off) for off in (0, 5) for p in range(len(odd))]
+    cache = fresh_cache(L, rng, len(runs), H, page, D)
+    slots = []
+    for n, (p, off) in enumerate(runs):
+        for s in (cache.kscale, cache.vscale):
+            s[n] = float(np.float32(odd[p]))
+        slots += [n * page + off + k for k in range(3)] + [-1]
+    x = random_tokens(rng, len(slots), 2 * H, D, "plain").cuda()
+    want = []
+    for part, c, s in ((x[:, :H], cache.kcodes, cache.kscale), (x[:, H:], cache.vcodes, cache.vscale)):
+        scale = s.cpu().numpy()
+        want.append(oracle.kv_append(np64(part), slots, c.cpu().numpy(),
+                                     np.where(np.isfinite(scale) & (scale >= 0), scale, np.float32(0)), page))
+    cache.append(x[:, :H], x[:, H:], i32(slots))
+    for (codes, scale), (c, s) in zip(want, ((cache.kcodes, cache.kscale), (cache.vcodes, cache.vscale))):
+        assert np.array_equal(s.cpu().numpy(), scale) and np.array_equal(c.cpu().numpy(), codes)
