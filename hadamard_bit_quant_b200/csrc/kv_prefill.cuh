@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
     if (ok && !*abort) {
       tc::tc_fence_after();
       const bool some = l > 0.f || l != l;
-      const float inv = over(l) * exp2_fast(m - ref);
+      const float root = exp2_fast(0.5f * (m - ref)), inv = over(l) * root;    // 2^(m - ref) itself may have no place in fp32
       const size_t out = (size_t)(rq.row0 + tok) * a.Hq + head;
       // Each lane has a row; through the place of the half's queries, whose last use is over, a warp's stores become whole
       // lines (two or four rows at a time).
@@ -470,8 +470,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
           uint32_t y[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float e0 = some ? __uint_as_float(x[8 * k + 2 * i]) * inv : 0.f;
-            const float e1 = some ? __uint_as_float(x[8 * k + 2 * i + 1]) * inv : 0.f;
+            const float e0 = some ? __uint_as_float(x[8 * k + 2 * i]) * inv * root : 0.f;
+            const float e1 = some ? __uint_as_float(x[8 * k + 2 * i + 1]) * inv * root : 0.f;
             y[i] = (uint32_t)float_to_bf16_bits(e0) | ((uint32_t)float_to_bf16_bits(e1) << 16);
           }
           const int ch = 4 * c + k;
