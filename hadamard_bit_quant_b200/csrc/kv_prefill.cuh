@@ -43,8 +43,8 @@ template <int D> struct __align__(1024) PreSmem {
   uint8_t q[2][kPanels][128 * 128];
   uint8_t k[2][kPanels][kPreKeys * 128];
   uint8_t v[2][kPanels][kPreKeys * 128];
-  // of each tile: [0, 8) key scales of the 16-key groups, [8, 16) log2 of their value scales, [16, 24) the inverses of
-  // those, [24] bits: the groups that are not in the cache, and from kPreApart the two steps
+  // of each tile: [0, 8) key scales of the 16-key groups, [8, 16) log2 of their value scales, [16] bits: the groups that
+  // are not in the cache, and from kPreApart the two steps
   float scale[kPreRing][32];
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2], p_full[2][2], o_full[2], o_last[2];
   uint64_t drained[2];
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
       HBL_TMEM_LD32(src + 32u, (x + 32));
       const uint32_t sc = tc::su32(&S.scale[(j - lo) % kPreRing][0]) + 16u * (n & 1);
       const uint4 kq = lds128(sc), vq = lds128(sc + 32);
-      const uint32_t bits = __float_as_uint(S.scale[(j - lo) % kPreRing][24]);
+      const uint32_t bits = __float_as_uint(S.scale[(j - lo) % kPreRing][16]);
       const uint32_t bad = (bits >> (kPreStepGroups * (n & 1))) & 15u;
       // never zero, so that a masked score (minus infinity) stays one when it is multiplied
       const float least = 1.17549435e-38f;
@@ -357,13 +357,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
                           fmaxf(__uint_as_float(kq.z) * qs, least), fmaxf(__uint_as_float(kq.w) * qs, least)};
       // addends of the exponent, relative to the reference; see kSpread
       float add[4];
-      auto addends = [&](const uint4& lv, float lowest) {
+      auto addends = [&](const uint4& lv) {
+        const float lowest = -ref - kSpread;
         add[0] = fmaxf(__uint_as_float(lv.x) - m, lowest);
         add[1] = fmaxf(__uint_as_float(lv.y) - m, lowest);
         add[2] = fmaxf(__uint_as_float(lv.z) - m, lowest);
         add[3] = fmaxf(__uint_as_float(lv.w) - m, lowest);
       };
-      addends(vq, -INFINITY);
+      addends(vq);
       tc::tc_wait_ld();
       if (!(key0 >= lane_lo && key0 + kPreStep <= lane_hi && bad == 0)) {
         const int c_lo = first - key0, c_hi = last - key0;      // the columns that this row sees
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
         l *= exp2_fast(ref - rn);
         m = mn;
         ref = rn;
-        addends(lv, -ref - kSpread);
+        addends(lv);
         if (n > 0 && __any_sync(0xffffffffu, ao != 1.f)) {
           // Once the products so far are complete. Those up to the last but one are (this step's scores were issued behind
           // them), and the next one waits for this step, so the phase is either this one or just over.
@@ -410,12 +411,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
           }
         }
       }
-      // From weights to p: a block's 1 / s, and the references; 2^88 at most (see kSpread), also where this is infinity times
-      // zero, a row that has seen scales of 0 alone.
-      const float kappa = exp2_fast(m - ref), most_back = __uint_as_float((127u + (uint32_t)kSpread) << 23);
-      const uint4 iq = lds128(sc + 64);
-      const float back[4] = {fminf(__uint_as_float(iq.x) * kappa, most_back), fminf(__uint_as_float(iq.y) * kappa, most_back),
-                             fminf(__uint_as_float(iq.z) * kappa, most_back), fminf(__uint_as_float(iq.w) * kappa, most_back)};
+      // from weights to p: a block's 1 / s, and the references
+      const float back[4] = {exp2_fast(-ref - add[0]), exp2_fast(-ref - add[1]), exp2_fast(-ref - add[2]), exp2_fast(-ref - add[3])};
       // A pair's exponentials take the special function unit 16 cycles; the arithmetic of the pair kLag in front is issued
       // in their shadow, in this order, and never waits for them.
       constexpr int kPairs = kPreStep / 2, kLag = 4;
@@ -667,9 +664,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const AttnAr
           float* dst = S.scale[n % kPreRing];
           dst[lane] = ks;
           dst[8 + lane] = lv;
-          dst[16 + lane] = exp2_fast(-lv);
           if (lane == 0) {
-            dst[24] = __uint_as_float(bad | (apart & 0x0fu ? 1u << kPreApart : 0u) | (apart & 0xf0u ? 2u << kPreApart : 0u));
+            dst[16] = __uint_as_float(bad | (apart & 0x0fu ? 1u << kPreApart : 0u) | (apart & 0xf0u ? 2u << kPreApart : 0u));
             if (bad) set_device_error(HBL_ERR_INVALID_ARG);
           }
         }
