@@ -181,7 +181,10 @@ class KVCache:
         return st if T > 1 else H * D
 
     def append(self, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
-        """Quantise K and V (bf16 [T, kv_heads, head_dim], e.g. parts of one projection's output) into their slots."""
+        """Quantise K and V (bf16 [T, kv_heads, head_dim], e.g. parts of one projection's output) into their slots.
+
+        A louder token raises its block's scale for good, also where ``KVPages.plan`` drops it again.
+        """
         _index(slots)
         assert slots.get_device() == self.kcodes.get_device()
         ks, vs = self._rows(K, self.kv_heads), self._rows(V, self.kv_heads)
@@ -212,7 +215,8 @@ class KVCache:
         """Attention of Q (bf16 [T, heads, head_dim]) over the cache: out, or (out, lse) with ``return_lse``.
 
         Request b's rows are cu_q[b] .. cu_q[b + 1], its cache kv_lens[b] tokens in the pages block_table[b].
-        scale: 1 / sqrt(head_dim) unless given.
+        scale: 1 / sqrt(head_dim) unless given. Rows of no request, and of one with more than max_q, are not written: what
+        ``out`` and ``lse`` held, or anything where they are not given.
         """
         _index(cu_q, kv_lens, block_table)
         stride = self._rows(Q)

@@ -295,7 +295,8 @@ int hbl_quantize_qkv(const hbl_bf16* X, int T, int H, int d, int bits, int bos_t
  *                this step are handed out first (in the order of requests and
  *                pages), then the stack from its top; what is left of them is
  *                pushed with the first on top, so that dropping what a step
- *                added restores the stack.
+ *                added restores the stack (not what appending its tokens did
+ *                to the blocks: see hbl_kv_append).
  *   free_count : device int32 1, in/out.
  *   cu_q       : device int32 B + 1, written: rows of each request's new
  *                tokens (prefix sums of max(new_lens, 0), cut at T).
@@ -326,6 +327,11 @@ int hbl_kv_plan(const int32_t* new_lens, int B, int page, int num_pages, int max
  * new ones rint(x / s) (exact quotients, ties to even). NaN is stored as 0, an
  * infinity as the largest finite value. Tokens that a page held behind the
  * run are no longer valid. In one call a page may be named by one run only.
+ * A block's scale never falls while the page is in use: tokens that are dropped
+ * again (hbl_kv_plan) leave it as they raised it, with the codes before them
+ * rescaled, so a loud rejected draft coarsens what stays in its last page. And
+ * codes depend on how tokens come: a page filled token by token is rounded
+ * once for each rise of its scale, one that is filled at once a single time.
  * T * Hkv < 2^31.
  */
 int hbl_kv_append(const hbl_bf16* K, const hbl_bf16* V, int T, int Hkv, int D, long long k_stride,

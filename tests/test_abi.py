@@ -159,3 +159,24 @@ def kv_attention_args(**kw):
 ])
 def test_kv_attention_argument_checks(lib, kw, status):
     assert lib.hbl_kv_attention(*kv_attention_args(**kw)) == status
+
+
+def test_kv_cache_argument_checks(lib):
+    plan = lambda new=BAD, B=2, page=16, num=20, width=8, T=4, state=BAD, slots=BAD: lib.hbl_kv_plan(   # noqa: E731
+        new, B, page, num, width, T, state, BAD, BAD, BAD, BAD, slots, BAD, None)
+    assert plan(page=24) == plan(num=0) == plan(num=1 << 27) == plan(B=8193) == plan(B=-1) == plan(T=-1) == 2
+    assert plan(width=0) == plan(width=1 << 28) == plan(B=8192, width=1 << 18) == 2
+    assert plan(new=None) == plan(state=None) == plan(slots=None) == plan(new=BAD + 1) == plan(slots=BAD + 2) == 1
+    assert plan(B=0, new=None) == 0
+    append = lambda K=BAD, T=4, H=2, D=64, stride=256, slots=BAD, page=16, num=20, codes=BAD, scale=BAD: lib.hbl_kv_append(  # noqa: E731
+        K, BAD, T, H, D, stride, 256, slots, page, num, codes, BAD, scale, BAD, None)
+    assert append(page=8) == append(D=32) == append(H=0) == append(H=65536) == append(T=-1) == append(T=1 << 30) == 2
+    assert append(stride=120) == append(stride=260) == append(num=-1) == 2
+    assert append(K=None) == append(slots=None) == append(codes=None) == append(scale=None) == 1
+    assert append(K=BAD + 8) == append(slots=BAD + 1) == append(codes=BAD + 4) == append(scale=BAD + 2) == 1
+    assert append(T=0, K=None, slots=None) == 0
+    read = lambda slots=BAD, T=4, D=64, K=BAD, V=BAD, codes=BAD, scale=BAD: lib.hbl_kv_read(            # noqa: E731
+        slots, T, 2, D, 16, 20, codes, BAD, scale, BAD, K, V, None)
+    assert read(D=80) == read(T=-1) == 2
+    assert read(slots=None) == read(codes=None) == read(scale=None) == read(K=BAD + 8) == read(V=BAD + 2) == 1
+    assert read(T=0) == read(K=None, V=None) == 0

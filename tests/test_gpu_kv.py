@@ -952,3 +952,20 @@ def test_attention_output_of_one_faint_key(L, q, Hq, Hkv, D, page, many, below):
     cache.kcodes[int(table[0, 0])] = 128
     check_rows(case, lag=-7)
     check_rows(case, lag=-7, causal=False)
+
+
+def test_dropped_tokens_leave_their_scale(L):
+    """A rejected draft: lengths and pages go back, the block it was in keeps the scale that it was raised to."""
+    H, D, page = 2, 64, 16
+    pages, cache = L.KVPages.empty(1, 2, 4, page), L.KVCache.empty(4, H, page, D)
+    x = random_tokens(np.random.default_rng(43), 12, H, D, "plain").cuda()
+    step = pages.plan(i32([6]), 6)
+    cache.append(x[:6], x[:6], step.slots)
+    codes, scale = (c.clone() for c in (cache.kcodes, cache.kscale))
+    step = pages.plan(i32([3]), 3)
+    cache.append(x[6:9] * 50, x[6:9] * 50, step.slots)
+    pages.plan(i32([-3]), 0)
+    assert pages.kv_lens.tolist() == [6] and pages.free_count.tolist() == [3]
+    want, raised = oracle.kv_append(np64(x[6:9] * 50), [6, 7, 8], codes.cpu().numpy(), scale.cpu().numpy(), page)
+    assert np.array_equal(cache.kcodes[0, :, :6].cpu().numpy(), want[0, :, :6]) and np.array_equal(cache.kscale.cpu().numpy(), raised)
+    assert bool((cache.kscale[0] > 10 * scale[0]).all())
