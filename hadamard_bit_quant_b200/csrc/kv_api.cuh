@@ -49,13 +49,14 @@ KvWs kv_ws_layout(int B, int D) {
 // cache; more go to the tensor-core kernel, which reads it once for 256 rows but gives a request's head to one CTA.
 constexpr int kFewRows = 32;
 
-// Rows of all query heads together up to which that holds for every request. Measured, tensor-core kernel / this one, us: 8
-// rows of 64 heads on 8 over 131072 keys (512 in all): 1771 / 231; 512 rows of 8 heads over 8192 (4096): 156 / 121; 64
-// rows of 32 over 32768 (2048): 457 / 240; 2048 rows of 4 over 2048 (8192): 50 / 78; 1024 rows of 8 over 1024 (8192): 28 / 31.
+// Rows of all query heads together up to which that holds for every request. Measured for one request, tensor-core kernel / this
+// one, us: 8 rows of 64 heads on 8 over 131072 keys (512 in all): 1720 / 244; 64 rows of 32 on 8 over 32768 (2048): 616 / 238; 512
+// rows of 8 on 2 over 8192 (4096): 162 / 126; 192 rows of 32 on 8 over 4096 (6144): 89 / 107; 1024 rows of 8 on 2 over 1024
+// (8192): 34 / 53; 2048 rows of 4 on 1 over 2048 (8192): 52 / 76.
 constexpr int kFewInAll = 6144;
 
 // Most cached tokens of a request, and most CTAs, for which kv_attn_kernel leaves each item to one CTA: one request of 130
-// tokens, 32 heads of 128, takes 4.9 us so and 10.9 us with the parts joined by a second kernel.
+// tokens, 32 heads of 128, takes 4.4 us so and 8.1 us with the parts joined by a second kernel.
 constexpr int kWholeKeys = 512, kWholeCtas = 4096;
 
 // Three kernels, each of which takes the requests that are its own: which those are is known on the GPU only.

@@ -24,10 +24,10 @@
 // reference, and the log2 of the sums. A run that is only a part of its row's keys goes to the workspace in the same form,
 // and kv_combine_kernel joins the parts.
 // Measured, of HBM's copy rate on the codes, queries and outputs: 128 requests of up to 4096 tokens, 32 query heads on 8 of
-// 128: 143 us, 5.6 TB/s (86 %); one of 131072: 56 us, 4.8 TB/s (73 %); 16 of up to 2048, 32 heads each their own: 43 us,
-// 4.5 TB/s (69 %). What is left there is the start (lengths, table, first tiles: 4 us one after the other), the
+// 128: 143 us, 5.6 TB/s (86 %); one of 131072: 57 us, 4.7 TB/s (72 %); 16 of up to 2048, 32 heads each their own: 44.5 us,
+// 4.35 TB/s (66 %). What is left there is the start (lengths, table, first tiles: 4 us one after the other), the
 // SMs' unequal share of the bandwidth (42 to 64 us for equal work) and the joining (3 us). Many short requests are
-// bound by the instructions at the beginnings and ends of runs: 2048 of 100 tokens 197 us where the bytes take 64.
+// bound by the instructions at the beginnings and ends of runs: 2048 of 100 tokens 195 us where the bytes take 64.
 #pragma once
 #include "hbl_common.cuh"
 #include <cuda_fp16.h>
@@ -184,7 +184,7 @@ HBL_DEVINL void row_power(float amax, float* up, float* down) {
 template <int D> struct AttnCfg {
   // Warps of a block and blocks of an SM. Twelve warps hold enough bytes in flight; more and smaller blocks hide each
   // other's beginnings and ends of runs, but leave more parts to be joined. Measured, 6 x 2 against 4 x 3: D = 64, 32
-  // requests of 5 rows, windows of 1024: 29.4 / 26.2 us; D = 128, one request of 131072: 56.9 / 58.7 us.
+  // requests of 5 rows, windows of 1024: 27.4 / 24.8 us; D = 128, one request of 131072: 56.2 / 57.1 us.
   static constexpr int kWarps = D == 64 ? 4 : 6, kCtas = 12 / kWarps;
   static constexpr int kKBytes = kAttnTile * D;
   static constexpr int kStageBytes = 2 * kKBytes + 16;

@@ -15,10 +15,10 @@
 // a reference of their own row, 2^7 below the largest. It is raised only when that has grown by 2^8, so the outputs in
 // TMEM are rarely rescaled; weights stay below 2^15 and are rounded to fp16. The sum of the p is fp32, relative to a
 // reference of the scores alone: each group's weights times 1 / s. Nothing that a row does not see has a part in its result.
-// Measured: 2048-row chunks of four requests over up to 8192 keys, 32 query heads on 8 of 128: 710 us, 896 TFLOP/s (54 % of
-// the burst cuBLAS rate, 64 % of the sustained one, at 990 W); one prompt of 2048, 32 heads of their own: 67 us, of which
-// 9 us for each 256-row item are its beginning and end. A step of 64 keys takes 2280 cycles, of which the tensor cores work
-// 1264 (QK with N = 64 is bound by its shared-memory operands, 49 cycles an instruction) and the special function units 1024;
+// Measured: 2048-row chunks of four requests over up to 8192 keys, 32 query heads on 8 of 128: 735 us, 865 TFLOP/s (52 % of
+// the burst cuBLAS rate, 62 % of the sustained one); one prompt of 2048, 32 heads of their own: 69 us, of which
+// 9 us for each 256-row item are its beginning and end. A step of 64 keys takes 2340 cycles, of which the tensor cores work
+// 1264 (QK with N = 64 is bound by its shared-memory operands, 49 cycles an instruction) and the special function units 1090;
 // a scheduler has two softmax warps, a converting one and an issuing one, and what is left is their latencies:
 // without the exponentials the kernel would take 14 % less, without the maxima 10 %, without QK 8 %, without the loads 6 %.
 // Every wait is bounded, as in gemm_tc.cuh.
